@@ -11,25 +11,13 @@
 #include <cuda_runtime.h>
 
 #include "bcjr.h"
+#include "bcjr_host.h"
 #include "bcjr_kernels.cuh"
 #include "bcjr_l16.cuh"
 #include "bcjr_l16c.cuh"
 #include "bcjr_l16v2.cuh"
 
 namespace {
-
-using bcjr::SweepParams;
-using bcjr::ViterbiParams;
-
-constexpr int kMaxL = 16;
-constexpr int kMaxD = 6;
-constexpr int64_t kMaxLen = 8192;
-constexpr size_t kMaxDynSmem = 227 * 1024;
-
-struct Shape {
-  int L, k, V, D, B, J, S, n;
-  int64_t n_seq, len;
-};
 
 bool fault_alloc() {
   const char* e = std::getenv("BCJR_FAULT_ALLOC");
@@ -38,7 +26,6 @@ bool fault_alloc() {
 
 // Kernels this library has launched in the process (bcjr_launch_count).
 std::atomic<uint64_t> g_launch_count{0};
-void counted_launch(int n = 1) { g_launch_count.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 // Library-private stream-ordered pool per device.  Scratch freed at the end of
 // a call stays mapped in the pool (release threshold = unlimited), so the next
@@ -46,6 +33,13 @@ void counted_launch(int n = 1) { g_launch_count.fetch_add((uint64_t)n, std::memo
 constexpr int kMaxPoolDevices = 64;
 std::mutex g_pool_mu;
 cudaMemPool_t g_pool[kMaxPoolDevices] = {};
+
+}  // namespace
+
+namespace bcjr {
+namespace host {
+
+void counted_launch(int n) { g_launch_count.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 int scratch_alloc(void** mem, size_t bytes, cudaStream_t st) {
   if (fault_alloc()) return BCJR_ERR_CUDA;
@@ -93,6 +87,25 @@ int check_dev_ptr(const void* p, bool nullable) {
   return BCJR_OK;
 }
 
+}  // namespace host
+}  // namespace bcjr
+
+namespace {
+
+using namespace bcjr::host;
+using bcjr::SweepParams;
+using bcjr::ViterbiParams;
+
+constexpr int kMaxL = 16;
+constexpr int kMaxD = 6;
+constexpr int64_t kMaxLen = 8192;
+constexpr size_t kMaxDynSmem = 227 * 1024;
+
+struct Shape {
+  int L, k, V, D, B, J, S, n;
+  int64_t n_seq, len;
+};
+
 int check_shape(int64_t n_seq, int64_t len, int L, int k, int V, Shape* sh) {
   if (n_seq < 0 || len < 1 || k < 1 || V < 1 || L < 1) return BCJR_ERR_INVALID_ARG;
   if (len % V != 0) return BCJR_ERR_INVALID_ARG;
@@ -115,19 +128,6 @@ bool generic_only() {
 }
 
 int check_T(float T) { return (std::isfinite(T) && T > 0.f) ? BCJR_OK : BCJR_ERR_INVALID_ARG; }
-
-// Carves one stream-ordered allocation into 256-byte aligned pieces.
-struct Arena {
-  size_t off = 0;
-  char* base = nullptr;
-  template <class T>
-  T* take(size_t count) {
-    size_t bytes = (count * sizeof(T) + 255) & ~size_t(255);
-    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
-    off += bytes;
-    return p;
-  }
-};
 
 // Generic kernels: about 32 states per thread per step (J groups of B members),
 // 32 to 512 threads.  Small trellises then run several small CTAs per SM instead
@@ -779,6 +779,9 @@ int bcjr_get_device_error(void* stream) {
   int flag = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&flag, bcjr::g_device_error, sizeof(int)) != cudaSuccess) return BCJR_ERR_CUDA;
   if (flag != 0 && cudaMemcpyToSymbol(bcjr::g_device_error, &zero, sizeof(int)) != cudaSuccess) return BCJR_ERR_CUDA;
+  int dense = 0;
+  if (int rc = take_dense_error(&dense)) return rc;
+  if (flag == 0) flag = dense;
   return flag;
 }
 

@@ -1,0 +1,453 @@
+// Host side of the layer-wise QAT operators declared in include/bcjr.h: 8-bit
+// block quantisation, the block-scaled product, Newton-Schulz orthogonalisation
+// and the Muon step.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bcjr.h"
+#include "bcjr_gemm.cuh"
+#include "bcjr_host.h"
+#include "bcjr_quant.cuh"
+
+namespace bcjr {
+namespace host {
+
+int take_dense_error(int* flag) {
+  int zero = 0;
+  if (cudaMemcpyFromSymbol(flag, gemm::g_dense_error, sizeof(int)) != cudaSuccess) return BCJR_ERR_CUDA;
+  if (*flag != 0 && cudaMemcpyToSymbol(gemm::g_dense_error, &zero, sizeof(int)) != cudaSuccess) return BCJR_ERR_CUDA;
+  return BCJR_OK;
+}
+
+}  // namespace host
+}  // namespace bcjr
+
+namespace {
+
+using namespace bcjr::host;
+namespace G = bcjr::gemm;
+namespace Q = bcjr::quant;
+
+static_assert(G::kErrTimeout == BCJR_ERR_TIMEOUT, "device and host status codes agree");
+static_assert((int)G::OUT_F32 == BCJR_F32 && (int)G::OUT_F16 == BCJR_F16 && (int)G::OUT_BF16 == BCJR_BF16, "output types");
+static_assert((int)Q::IN_F32 == BCJR_F32 && (int)Q::IN_F16 == BCJR_F16 && (int)Q::IN_BF16 == BCJR_BF16, "input types");
+
+constexpr int64_t kMaxExtent = (int64_t)1 << 30;
+constexpr int64_t kMaxMatrix = 65536;   // orthogonalise: rows and columns
+constexpr int64_t kMaxBatch = 65535;
+constexpr int kMaxSteps = 64;
+
+// A device or managed pointer of the current device, aligned to `align` bytes.
+int check_ptr(const void* p, size_t align) {
+  if (p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0) return BCJR_ERR_INVALID_ARG;
+  cudaPointerAttributes a;
+  int dev = 0;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_INVALID_ARG;
+  }
+  if (a.type == cudaMemoryTypeManaged) return BCJR_OK;
+  return a.type == cudaMemoryTypeDevice && a.device == dev ? BCJR_OK : BCJR_ERR_INVALID_ARG;
+}
+
+bool is_wide(int t) { return t == BCJR_F32 || t == BCJR_F16 || t == BCJR_BF16; }
+bool is_8bit(int t) { return t == BCJR_E4M3 || t == BCJR_E5M2; }
+size_t size_of(int t) { return t == BCJR_F32 ? 4 : is_8bit(t) ? 1 : 2; }
+int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t parts(int64_t n, int64_t m) { return (n + m - 1) / m; }
+
+int sm_count(int* n) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
+  return BCJR_OK;
+}
+
+// cuTensorMapEncodeTiled through the runtime (the library does not link against the driver).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) == cudaSuccess &&
+        st == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+    else
+      cudaGetLastError();
+  }
+  return fn;
+}
+
+// One operand of a product: [batch][outer][inner], rows of `ld` elements.
+struct Operand {
+  const void* p;
+  int64_t inner, outer, ld, batch, batch_stride;
+};
+
+// Copies of 128 bytes (inner) x `box` rows, 128-byte swizzle, zeros outside.
+int make_map(CUtensorMap* map, const Operand& o, int elem, int box) {
+  EncodeFn fn = encode_fn();
+  if (fn == nullptr) return BCJR_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)o.batch};
+  const int64_t row = o.outer > 1 ? o.ld * elem : up(o.inner * elem, 16);
+  const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)(o.batch > 1 ? o.batch_stride * elem : row * o.outer)};
+  const cuuint32_t boxes[3] = {(cuuint32_t)(128 / elem), (cuuint32_t)box, 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = fn(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(o.p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BCJR_OK : BCJR_ERR_CUDA;
+}
+
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+int launch_tile(const Operand& r, const Operand& c, G::Params p, int64_t tiles, int64_t batch, cudaStream_t st) {
+  using S = G::Shape<KIND, BN>;
+  constexpr int elem = KIND == G::MX ? 1 : 2;
+  CUtensorMap mr, mc;
+  if (int rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) return rc;
+  if (int rc = make_map(&mc, c, elem, C_MN ? 64 : BN)) return rc;
+  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.splits), 1, (unsigned)batch);
+  cfg.blockDim = dim3(G::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, mr, mc, p) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
+  counted_launch();
+  return BCJR_OK;
+}
+
+// Blocks of one tile: as many (1, 2, 4 or 8) as the tiles leave room for, each with at least two stages of k.
+int splits_for(int64_t tiles, int64_t stages, int nsm) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= nsm && stages >= s * 4) s *= 2;
+  return s;
+}
+
+// ------------------------------------------------------------ 8-bit product
+
+template <int BN>
+int matmul_bn(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
+  const int64_t tiles = parts(p.rows, G::kRowsTile) * parts(p.cols, BN);
+  if (tiles * 8 > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
+  p.tiles_r = (int)parts(p.rows, G::kRowsTile);
+  p.splits = splits_for(tiles, parts(p.k, 128), nsm);
+  return launch_tile<G::MX, BN, false, false, G::OUT>(r, c, p, tiles, 1, st);
+}
+
+int run_matmul(const Operand& r, const Operand& c, const G::Params& p, cudaStream_t st) {
+  int nsm = 0;
+  if (int rc = sm_count(&nsm)) return rc;
+  if (p.cols <= 16) return matmul_bn<16>(r, c, p, nsm, st);
+  if (p.cols <= 32) return matmul_bn<32>(r, c, p, nsm, st);
+  if (p.cols <= 64) return matmul_bn<64>(r, c, p, nsm, st);
+  if (p.cols <= 128 || parts(p.rows, 128) * parts(p.cols, 256) < nsm) return matmul_bn<128>(r, c, p, nsm, st);
+  return matmul_bn<256>(r, c, p, nsm, st);
+}
+
+// ------------------------------------------------------------ Newton-Schulz
+
+constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// The iterates are kept in fp16 with headroom for entries up to 16; the singular
+// values of u / |u| lie in [0, 1].  False if the coefficients drive a singular
+// value (sampled over the interval that each step can reach) above 2.
+bool coeffs_bounded(const float* co, int steps) {
+  double top = 1.0;
+  for (int s = 0; s < steps; ++s) {
+    const double a = co[3 * s], b = co[3 * s + 1], c = co[3 * s + 2];
+    double most = 0.0, inner = 0.0;
+    for (int i = 0; i <= 256; ++i) {
+      const double x = top * i / 256.0, t = x * x;
+      most = std::max(most, std::fabs(x * (a + t * (b + t * c))));
+      inner = std::max(inner, std::fabs(t * (b + t * c)));
+    }
+    if (!(most <= 2.0) || !(inner <= 8.0)) return false;
+    top = most;
+  }
+  return true;
+}
+
+struct Shape2 {
+  int64_t batch, rows, cols;
+};
+
+int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps) {
+  if (sh.batch < 0 || sh.rows < 0 || sh.cols < 0) return BCJR_ERR_INVALID_ARG;
+  if (steps < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return BCJR_ERR_INVALID_ARG;
+  if (steps > kMaxSteps || sh.rows > kMaxMatrix || sh.cols > kMaxMatrix || sh.batch > kMaxBatch) return BCJR_ERR_UNSUPPORTED;
+  if (coeffs != nullptr && !coeffs_bounded(coeffs, steps)) return BCJR_ERR_INVALID_ARG;
+  return BCJR_OK;
+}
+
+template <int BN, int EPI, bool MN>
+int sym_bn(const Operand& x, G::Params p, int64_t batch, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, 128), tiles = (128 / BN) * t * (t + 1) / 2;
+  p.tiles_r = (int)t;
+  p.splits = splits_for(tiles * batch, parts(p.k, 64), nsm);
+  return launch_tile<G::F16, BN, MN, MN, EPI>(x, x, p, tiles, batch, st);
+}
+template <int EPI, bool MN>
+int run_sym(const Operand& x, const G::Params& p, int64_t batch, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, 128);
+  if (t * (t + 1) / 2 * batch * 2 < nsm) return sym_bn<64, EPI, MN>(x, p, batch, nsm, st);
+  return sym_bn<128, EPI, MN>(x, p, batch, nsm, st);
+}
+
+template <int BN, int EPI, bool R_MN>
+int iter_bn(const Operand& r, const Operand& c, G::Params p, int64_t batch, int nsm, cudaStream_t st) {
+  p.tiles_r = (int)parts(p.rows, 128);
+  const int64_t tiles = p.tiles_r * parts(p.cols, BN);
+  p.splits = splits_for(tiles * batch, parts(p.k, 64), nsm);
+  return launch_tile<G::F16, BN, R_MN, false, EPI>(r, c, p, tiles, batch, st);
+}
+template <int EPI, bool R_MN>
+int run_iter(const Operand& r, const Operand& c, const G::Params& p, int64_t batch, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, 128);
+  if (p.cols <= 64 || t * parts(p.cols, 128) * batch * 2 < nsm) return iter_bn<64, EPI, R_MN>(r, c, p, batch, nsm, st);
+  if (p.cols <= 128 || t * parts(p.cols, 256) * batch < nsm) return iter_bn<128, EPI, R_MN>(r, c, p, batch, nsm, st);
+  return iter_bn<256, EPI, R_MN>(r, c, p, batch, nsm, st);
+}
+
+template <int T>
+void launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
+  Q::norm_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), 256, 0, st>>>(u);
+  Q::start_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), 256, 0, st>>>(u);
+  counted_launch(2);
+}
+
+// The whole iteration; `last` holds the epilogue of the last product (out, its
+// layout and type, the weights' factors) and says which by `epi`.
+int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi,
+                      const G::Params& last, cudaStream_t st) {
+  int nsm = 0;
+  if (int rc = sm_count(&nsm)) return rc;
+  const bool tall = sh.rows > sh.cols;
+  const int64_t m = std::min(sh.rows, sh.cols);
+  const int64_t ld_x = up(sh.cols, 8), ld_p = up(m, 8);
+  const int64_t nx = sh.rows * ld_x, np = m * ld_p;
+  u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(sh.rows * sh.cols, 1024), parts(4 * nsm, sh.batch)));
+  __half *x0, *x1, *pp, *bb;
+  double* partial;
+  auto layout = [&](Arena& ar) {
+    partial = ar.take<double>((size_t)(sh.batch * u.parts));
+    x0 = ar.take<__half>((size_t)(sh.batch * nx));
+    x1 = ar.take<__half>((size_t)(sh.batch * nx));
+    pp = ar.take<__half>((size_t)(sh.batch * np));
+    bb = ar.take<__half>((size_t)(sh.batch * np));
+  };
+  Arena sizing;
+  layout(sizing);
+  void* mem = nullptr;
+  if (int rc = scratch_alloc(&mem, sizing.off, st)) return rc;
+  Arena ar;
+  ar.base = static_cast<char*>(mem);
+  layout(ar);
+
+  u.partial = partial;
+  u.x = x0;
+  u.ld_x = ld_x;
+  u.batch_x = nx;
+  u.rows = (int)sh.rows;
+  u.cols = (int)sh.cols;
+  u.scale = G::kIterScale;
+  if (g_type == BCJR_F32) launch_update<Q::IN_F32>(u, sh.batch, st);
+  else if (g_type == BCJR_F16) launch_update<Q::IN_F16>(u, sh.batch, st);
+  else launch_update<Q::IN_BF16>(u, sh.batch, st);
+  int rc = cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA;
+
+  for (int s = 0; s < steps && rc == BCJR_OK; ++s) {
+    const float* co = coeffs != nullptr ? coeffs + 3 * s : kMuonCoeffs;
+    // X along its rows (inner = columns): the Gram matrix of the shorter side
+    // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
+    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch, nx};
+    G::Params p{};
+    p.rows = p.cols = (int)m;
+    p.k = (int)(tall ? sh.rows : sh.cols);
+    p.out = pp;
+    p.ld_out = ld_p;
+    p.batch_out = np;
+    rc = tall ? run_sym<G::GRAM, true>(x, p, sh.batch, nsm, st) : run_sym<G::GRAM, false>(x, p, sh.batch, nsm, st);
+    if (rc) break;
+    const Operand gram{pp, m, m, ld_p, sh.batch, np};
+    p.k = (int)m;
+    p.out = bb;
+    p.x = pp;
+    p.ld_x = ld_p;
+    p.batch_x = np;
+    p.fa = co[2];
+    p.fb = co[1];
+    if ((rc = run_sym<G::POLY, false>(gram, p, sh.batch, nsm, st))) break;
+    // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
+    const Operand poly{bb, m, m, ld_p, sh.batch, np};
+    const bool end = s + 1 == steps;
+    G::Params q = end ? last : G::Params{};
+    q.rows = (int)sh.cols;
+    q.cols = (int)sh.rows;
+    q.k = (int)m;
+    q.x = x0;
+    q.ld_x = ld_x;
+    q.batch_x = nx;
+    q.fa = 1.f;
+    q.fb = co[0];
+    if (!end) {
+      q.out = x1;
+      q.ld_out = ld_x;
+      q.batch_out = nx;
+    }
+#define BCJR_ITER(E) \
+  (tall ? run_iter<E, false>(poly, x, q, sh.batch, nsm, st) : run_iter<E, true>(x, poly, q, sh.batch, nsm, st))
+    rc = !end ? BCJR_ITER(G::ITER) : epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
+#undef BCJR_ITER
+    std::swap(x0, x1);
+  }
+  if (cudaFreeAsync(mem, st) != cudaSuccess && rc == BCJR_OK) rc = BCJR_ERR_CUDA;
+  return rc;
+}
+
+template <int T>
+int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int64_t tiles, cudaStream_t st) {
+  void (*kern)(Q::QuantParams) = e5m2 ? (row_blocks ? Q::quantise_kernel<T, true, true> : Q::quantise_kernel<T, true, false>)
+                                      : (row_blocks ? Q::quantise_kernel<T, false, true> : Q::quantise_kernel<T, false, false>);
+  kern<<<(unsigned)tiles, Q::kThreads, 0, st>>>(p);
+  counted_launch();
+  return cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bcjr_fp8_quantise(const void* x, int x_type, int64_t rows, int64_t cols, int64_t ld_x, const float* minus,
+                      int64_t ld_minus, int q_type, int block_rows, void* q, int64_t ld_q, void* scale,
+                      int64_t ld_scale, void* qt, int64_t ld_qt, void* scale_t, int64_t ld_scale_t, void* stream) {
+  if (rows < 0 || cols < 0 || !is_wide(x_type) || !is_8bit(q_type)) return BCJR_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != 128) return BCJR_ERR_INVALID_ARG;
+  if ((q == nullptr) != (scale == nullptr) || (qt == nullptr) != (scale_t == nullptr)) return BCJR_ERR_INVALID_ARG;
+  if (rows > kMaxExtent || cols > kMaxExtent) return BCJR_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return BCJR_OK;
+  if (q == nullptr && qt == nullptr) return BCJR_ERR_INVALID_ARG;
+  const int64_t tiles_r = parts(rows, 128), tiles_c = parts(cols, 128);
+  if (ld_x < cols || (minus != nullptr && ld_minus < cols)) return BCJR_ERR_INVALID_ARG;
+  if (q != nullptr && (ld_q < cols || ld_q % 16 != 0 || ld_scale < tiles_c)) return BCJR_ERR_INVALID_ARG;
+  if (qt != nullptr && (ld_qt < rows || ld_qt % 16 != 0 || ld_scale_t < tiles_r)) return BCJR_ERR_INVALID_ARG;
+  if (tiles_r * tiles_c > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
+  int rc;
+  if ((rc = check_ptr(x, size_of(x_type)))) return rc;
+  if (minus != nullptr && (rc = check_ptr(minus, 4))) return rc;
+  if (q != nullptr && ((rc = check_ptr(q, 16)) || (rc = check_ptr(scale, 1)))) return rc;
+  if (qt != nullptr && ((rc = check_ptr(qt, 16)) || (rc = check_ptr(scale_t, 1)))) return rc;
+  Q::QuantParams p{};
+  p.x = x; p.minus = minus;
+  p.q = static_cast<uint8_t*>(q); p.s = static_cast<uint8_t*>(scale);
+  p.qt = static_cast<uint8_t*>(qt); p.st = static_cast<uint8_t*>(scale_t);
+  p.ld_x = ld_x; p.ld_minus = ld_minus; p.ld_q = ld_q; p.ld_s = ld_scale; p.ld_qt = ld_qt; p.ld_st = ld_scale_t;
+  p.rows = (int)rows; p.cols = (int)cols; p.tiles_c = (int)tiles_c;
+  p.vec = ld_x % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * size_of(x_type)) == 0 &&
+          (minus == nullptr || (ld_minus % 4 == 0 && reinterpret_cast<uintptr_t>(minus) % 16 == 0));
+  const bool e5m2 = q_type == BCJR_E5M2;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (x_type == BCJR_F32) return launch_quantise<Q::IN_F32>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
+  if (x_type == BCJR_F16) return launch_quantise<Q::IN_F16>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
+  return launch_quantise<Q::IN_BF16>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
+}
+
+int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void* scale_a, int64_t ld_scale_a, int a_block_rows,
+                    const void* b, int b_type, int64_t ld_b, const void* scale_b, int64_t ld_scale_b, int b_block_rows,
+                    int64_t M, int64_t N, int64_t K, float alpha, void* out, int out_type, int64_t ld_out,
+                    void* stream) {
+  if (M < 0 || N < 0 || K < 0 || !is_8bit(a_type) || !is_8bit(b_type) || !is_wide(out_type)) return BCJR_ERR_INVALID_ARG;
+  if ((a_block_rows != 1 && a_block_rows != 128) || (b_block_rows != 1 && b_block_rows != 128)) return BCJR_ERR_INVALID_ARG;
+  if (!std::isfinite(alpha)) return BCJR_ERR_INVALID_ARG;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return BCJR_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return BCJR_OK;
+  if (ld_out < N) return BCJR_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_ptr(out, size_of(out_type)))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (K == 0)
+    return cudaMemset2DAsync(out, (size_t)ld_out * size_of(out_type), 0, (size_t)N * size_of(out_type), (size_t)M, st) == cudaSuccess
+               ? BCJR_OK
+               : BCJR_ERR_CUDA;
+  const int64_t kb = parts(K, 128);
+  if (ld_a < K || ld_a % 16 != 0 || ld_b < K || ld_b % 16 != 0 || ld_scale_a < kb || ld_scale_b < kb) return BCJR_ERR_INVALID_ARG;
+  if ((rc = check_ptr(a, 16)) || (rc = check_ptr(b, 16)) || (rc = check_ptr(scale_a, 1)) || (rc = check_ptr(scale_b, 1)))
+    return rc;
+  // r (the lanes) runs along the rows of out
+  const Operand r{b, K, N, ld_b, 1, 0}, c{a, K, M, ld_a, 1, 0};
+  G::Params p{};
+  p.rows = (int)N; p.cols = (int)M; p.k = (int)K;
+  p.sr = static_cast<const uint8_t*>(scale_b); p.sc = static_cast<const uint8_t*>(scale_a);
+  p.ld_sr = ld_scale_b; p.ld_sc = ld_scale_a;
+  p.shift_r = b_block_rows == 128 ? 7 : 0; p.shift_c = a_block_rows == 128 ? 7 : 0;
+  p.fmt_r = b_type == BCJR_E5M2 ? 1 : 0; p.fmt_c = a_type == BCJR_E5M2 ? 1 : 0;
+  p.out = out; p.ld_out = ld_out; p.out_type = out_type; p.fa = alpha;
+  return run_matmul(r, c, p, st);
+}
+
+int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g,
+                       int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out, int out_type,
+                       int64_t ld_out, int64_t batch_stride_out, void* stream) {
+  const Shape2 sh{batch, rows, cols};
+  int rc = check_iteration(sh, steps, coeffs, eps);
+  if (rc) return rc;
+  if (!is_wide(g_type) || (out_type != BCJR_F16 && out_type != BCJR_BF16)) return BCJR_ERR_INVALID_ARG;
+  if (batch == 0 || rows == 0 || cols == 0) return BCJR_OK;
+  if (ld_g < cols || ld_out < cols) return BCJR_ERR_INVALID_ARG;
+  if (batch > 1 && (batch_stride_g < 0 || batch_stride_out < (rows - 1) * ld_out + cols)) return BCJR_ERR_INVALID_ARG;
+  if ((rc = check_ptr(g, size_of(g_type))) || (rc = check_ptr(out, 2))) return rc;
+  Q::UpdateParams u{};
+  u.g = g; u.ld_g = ld_g; u.batch_g = batch_stride_g; u.eps = eps;
+  G::Params last{};
+  last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
+  return run_newton_schulz(sh, u, g_type, steps, coeffs, G::LAST, last, static_cast<cudaStream_t>(stream));
+}
+
+int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad, float* momentum,
+                   int64_t ld_momentum, int64_t rows, int64_t cols, float lr, float mu, int nesterov,
+                   float weight_decay, float scale, int steps, const float* coeffs, float eps, void* stream) {
+  const Shape2 sh{1, rows, cols};
+  int rc = check_iteration(sh, steps, coeffs, eps);
+  if (rc) return rc;
+  if (!is_wide(grad_type)) return BCJR_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || !std::isfinite(mu) || !std::isfinite(weight_decay) || !std::isfinite(scale)) return BCJR_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return BCJR_OK;
+  if (ld_w < cols || ld_grad < cols || ld_momentum < cols) return BCJR_ERR_INVALID_ARG;
+  if ((rc = check_ptr(w, 4)) || (rc = check_ptr(grad, size_of(grad_type))) || (rc = check_ptr(momentum, 4))) return rc;
+  Q::UpdateParams u{};
+  u.g = grad; u.ld_g = ld_grad; u.momentum = momentum; u.ld_m = ld_momentum;
+  u.mu = mu; u.nesterov = nesterov ? 1 : 0; u.eps = eps;
+  G::Params last{};
+  last.out = w; last.ld_out = ld_w;
+  last.keep = (float)(1.0 - (double)lr * (double)weight_decay);
+  last.rate = (float)((double)lr * (double)scale);
+  return run_newton_schulz(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,304 @@
+// 8-bit block quantisation and the elementwise passes of the Muon step.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace bcjr {
+namespace quant {
+
+enum InType { IN_F32 = 0, IN_F16 = 1, IN_BF16 = 2 };
+
+template <int T>
+struct In;
+template <>
+struct In<IN_F32> {
+  using type = float;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ void get4(const float* p, float (&v)[4]) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  }
+};
+template <>
+struct In<IN_F16> {
+  using type = __half;
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ void get4(const __half* p, float (&v)[4]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+};
+template <>
+struct In<IN_BF16> {
+  using type = __nv_bfloat16;
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  }
+};
+
+struct QuantParams {
+  const void* x;
+  const float* minus;          // or null
+  uint8_t *q, *s, *qt, *st;    // q and s, or qt and st, may be null
+  int64_t ld_x, ld_minus, ld_q, ld_s, ld_qt, ld_st;
+  int rows, cols, tiles_c;
+  int vec;                     // rows of x (and minus) start on 4-element boundaries
+};
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;
+
+// Exponent of the block's scale from the largest |x| as fp32 bits: the least
+// e >= -127 with |x| <= FMAX 2^e, FMAX = 0.875 * 2^TOP (448 or 57344), 0 for a
+// block of zeros, as the byte e + 127; 255 (NaN) if a value is not finite.
+// |x| = 1.m 2^(E - 127) fits 0.875 2^(TOP + e) if 1.m <= 1.75 and E - 126 <= TOP + e.
+template <int TOP>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
+  if (bits >= 0x7F800000u) return 255u;
+  if (bits == 0) return 127u;
+  const int e = (int)(bits >> 23) - 126 - TOP + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)(max(e, -127) + 127);
+}
+// 2^-e, exact (e >= -127 and e <= 128 - TOP), NaN for the byte 255.
+__device__ __forceinline__ float scale_factor(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((254u - byte) << 23);
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  uint16_t r;
+  if (E5M2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return codes2<E5M2>(a, b) | (codes2<E5M2>(c, d) << 16);
+}
+
+// One block takes one 128 x 128 tile of x: warp w the rows 16 w .. 16 w + 15,
+// lane l the columns 4 l .. 4 l + 3, so a tile is read once, in 16-byte loads
+// that are all in flight at once, and stays in registers for both layouts.  The
+// largest |x| of a row is one warp reduction on the fp32 bits (for values that
+// are not negative their order is the numbers' order, NaN above all); those of
+// the columns, or of the tile, meet in shared memory.  The codes of x^T go
+// through shared memory as words of four rows, word index xor (column / 4), so
+// that neither side has bank conflicts.
+// ROW_BLOCKS: one scale for each row (or column) and 128 values; else one for the tile.
+template <int T, bool E5M2, bool ROW_BLOCKS>
+__global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p) {
+  constexpr int TOP = E5M2 ? 16 : 9;
+  __shared__ uint32_t most[8][kTile];
+  __shared__ uint32_t words[kTile][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
+  const int r0 = tr * kTile + warp * 16, c0 = tc * kTile, c = c0 + 4 * lane;
+  const int live = min(16, p.rows - r0);            // rows of this warp, may be <= 0
+  using X = typename In<T>::type;
+  const X* x = static_cast<const X*>(p.x) + (int64_t)r0 * p.ld_x + c;
+  float v[16][4];
+  if (live == 16 && c + 4 <= p.cols && p.vec) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) In<T>::get4(x + (int64_t)i * p.ld_x, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[i][j] = (i < live && c + j < p.cols) ? In<T>::get(x[(int64_t)i * p.ld_x + j]) : 0.f;
+  }
+  if (p.minus != nullptr) {
+    const float* m = p.minus + (int64_t)r0 * p.ld_minus + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float u[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i < live) {
+        if (c + 4 <= p.cols && p.vec) {
+          In<IN_F32>::get4(m + (int64_t)i * p.ld_minus, u);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + j < p.cols) u[j] = m[(int64_t)i * p.ld_minus + j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = __fsub_rn(v[i][j], u[j]);
+    }
+  }
+
+  uint32_t col[4] = {0, 0, 0, 0};
+  uint32_t rowb[16];                                 // row scales as bytes
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b[j] = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
+      col[j] = max(col[j], b[j]);
+    }
+    if (ROW_BLOCKS && p.q != nullptr)
+      rowb[i] = scale_byte<TOP>(__reduce_max_sync(0xFFFFFFFFu, max(max(b[0], b[1]), max(b[2], b[3]))));
+  }
+  uint32_t tile_byte = 0;
+  if (!ROW_BLOCKS) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(max(col[0], col[1]), max(col[2], col[3])));
+    if (lane == 0) most[warp][0] = m;
+    __syncthreads();
+    uint32_t a = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) a = max(a, most[w][0]);
+    tile_byte = scale_byte<TOP>(a);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) rowb[i] = tile_byte;
+  }
+
+  if (p.q != nullptr) {
+    if (ROW_BLOCKS) {
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < live) p.s[(int64_t)(r0 + i) * p.ld_s + tc] = (uint8_t)rowb[i];
+      }
+    } else if (threadIdx.x == 0) {
+      p.s[(int64_t)tr * p.ld_s + tc] = (uint8_t)tile_byte;
+    }
+    uint8_t* q = p.q + (int64_t)r0 * p.ld_q + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i >= live) break;
+      const float f = scale_factor(rowb[i]);
+      const uint32_t w = codes4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
+      if (c + 4 <= p.cols) {
+        *reinterpret_cast<uint32_t*>(q + (int64_t)i * p.ld_q) = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (c + j < p.cols) q[(int64_t)i * p.ld_q + j] = (uint8_t)(w >> (8 * j));
+      }
+    }
+  }
+
+  if (p.qt != nullptr) {
+    uint32_t colb[4];
+    if (ROW_BLOCKS) {
+      *reinterpret_cast<uint4*>(&most[warp][4 * lane]) = make_uint4(col[0], col[1], col[2], col[3]);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) a = max(a, most[w][4 * lane + j]);
+        colb[j] = scale_byte<TOP>(a);
+        if (warp == 0 && c + j < p.cols) p.st[(int64_t)(c + j) * p.ld_st + tr] = (uint8_t)colb[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) colb[j] = tile_byte;
+      if (threadIdx.x == 0) p.st[(int64_t)tc * p.ld_st + tr] = (uint8_t)tile_byte;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = scale_factor(colb[j]);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        words[4 * lane + j][(warp * 4 + i / 4) ^ lane] = codes4<E5M2>(v[i][j] * f, v[i + 1][j] * f, v[i + 2][j] * f, v[i + 3][j] * f);
+    }
+    __syncthreads();
+    const int r = tr * kTile + 4 * lane;             // four rows of x, now columns
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int cl = warp * 16 + i;
+      if (c0 + cl >= p.cols) break;
+      const uint32_t w = words[cl][lane ^ (cl >> 2)];
+      uint8_t* q = p.qt + (int64_t)(c0 + cl) * p.ld_qt + r;
+      if (r + 4 <= p.rows) {
+        *reinterpret_cast<uint32_t*>(q) = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (r + j < p.rows) q[j] = (uint8_t)(w >> (8 * j));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ Muon's elementwise passes
+
+struct UpdateParams {
+  const void* g;
+  float* momentum;         // or null: the update is g itself
+  double* partial;         // [batch][parts]
+  __half* x;               // [batch][rows][ld_x]
+  int64_t ld_g, batch_g, ld_m, ld_x, batch_x;
+  int rows, cols, parts;
+  float mu;
+  int nesterov;
+  float eps, scale;
+};
+
+// u = g + mu momentum (nesterov) or momentum, from the momentum already updated; g without one.
+__device__ __forceinline__ float update_of(const UpdateParams& p, float g, float m) {
+  return p.nesterov ? fmaf(p.mu, m, g) : m;
+}
+
+// First pass: updates the momentum (in place) and leaves each block's sum of squares of u.
+template <int T>
+__global__ void __launch_bounds__(256) norm_kernel(const UpdateParams p) {
+  using X = typename In<T>::type;
+  __shared__ double part[8];
+  const int64_t n = (int64_t)p.rows * p.cols;
+  const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
+  double sum = 0.0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / p.cols, c = i - r * p.cols;
+    float u = In<T>::get(g[r * p.ld_g + c]);
+    if (p.momentum != nullptr) {
+      const float m = fmaf(p.mu, p.momentum[r * p.ld_m + c], u);
+      p.momentum[r * p.ld_m + c] = m;
+      u = update_of(p, u, m);
+    }
+    sum += (double)u * (double)u;
+  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) sum += part[w];
+    p.partial[(int64_t)blockIdx.y * p.parts + blockIdx.x] = sum;
+  }
+}
+
+// Second pass: X_0 = u / (|u| + eps), scaled, as fp16.
+template <int T>
+__global__ void __launch_bounds__(256) start_kernel(const UpdateParams p) {
+  using X = typename In<T>::type;
+  __shared__ float factor;
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < p.parts; i += 32) s += p.partial[(int64_t)blockIdx.y * p.parts + i];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (threadIdx.x == 0) factor = (float)((double)p.scale / (sqrt(s) + (double)p.eps));
+  }
+  __syncthreads();
+  const int64_t n = (int64_t)p.rows * p.cols;
+  const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
+  __half* x = p.x + blockIdx.y * p.batch_x;
+  const float f = factor;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / p.cols, c = i - r * p.cols;
+    float u = In<T>::get(g[r * p.ld_g + c]);
+    if (p.momentum != nullptr) u = update_of(p, u, p.momentum[r * p.ld_m + c]);
+    x[r * p.ld_x + c] = __float2half_rn(u * f);
+  }
+}
+
+}  // namespace quant
+}  // namespace bcjr

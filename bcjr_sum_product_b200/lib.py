@@ -6,10 +6,12 @@ is no CPU fallback: if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -24,6 +26,7 @@ BCJR_ERR_TIMEOUT = 4
 BCJR_ERR_NUMERIC = 5
 
 EXPORTS = ("bcjr_soft_codeword", "bcjr_vjp", "viterbi_decode", "bcjr_posterior_argmax",
+           "bcjr_fp8_quantise", "bcjr_fp8_matmul", "bcjr_orthogonalise", "bcjr_muon_step",
            "bcjr_get_device_error", "bcjr_launch_count", "bcjr_strerror", "bcjr_version")
 
 
@@ -54,6 +57,13 @@ def load(path: str = LIB_PATH):
             lib.viterbi_decode.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, P]
             lib.bcjr_posterior_argmax.argtypes = [P, i64, i64, i32, i32, i32, P, f32, P, P]
             lib.bcjr_qat_step.argtypes = [P, P, i64, i64, i32, i32, i32, P, f32, f32, f32, P, P, P, P, P]
+            lib.bcjr_fp8_quantise.argtypes = [P, i32, i64, i64, i64, P, i64, i32, i32, P, i64, P, i64, P, i64, P,
+                                              i64, P]
+            lib.bcjr_fp8_matmul.argtypes = [P, i32, i64, P, i64, i32, P, i32, i64, P, i64, i32, i64, i64, i64, f32, P,
+                                            i32, i64, P]
+            lib.bcjr_orthogonalise.argtypes = [P, i32, i64, i64, i64, i64, i64, i32, P, f32, P, i32, i64, i64, P]
+            lib.bcjr_muon_step.argtypes = [P, i64, P, i32, i64, P, i64, i64, i64, f32, f32, i32, f32, f32, i32, P, f32,
+                                           P]
             lib.bcjr_get_device_error.argtypes = [P]
             lib.bcjr_strerror.argtypes = [i32]
             lib.bcjr_strerror.restype = ctypes.c_char_p
@@ -62,7 +72,8 @@ def load(path: str = LIB_PATH):
             lib.bcjr_launch_count.argtypes = []
             lib.bcjr_launch_count.restype = ctypes.c_uint64
             for name in ("bcjr_soft_codeword", "bcjr_vjp", "viterbi_decode", "bcjr_posterior_argmax",
-                         "bcjr_qat_step", "bcjr_get_device_error"):
+                         "bcjr_qat_step", "bcjr_fp8_quantise", "bcjr_fp8_matmul", "bcjr_orthogonalise",
+                         "bcjr_muon_step", "bcjr_get_device_error"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -224,3 +235,203 @@ def soft_codeword_noalloc(w: torch.Tensor, codebook: torch.Tensor, L: int, k: in
             _stream(stream))
     _check(rc, "bcjr_soft_codeword_noalloc")
     return out_soft, out_logZ
+
+
+# ---------------------------------------------------------------- layer-wise QAT
+
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
+_WIDE = (torch.float32, torch.float16, torch.bfloat16)
+_CODES = (torch.float8_e4m3fn, torch.float8_e5m2)
+_BLOCK = 128
+#: Coefficients of Muon's Newton-Schulz step (the default of orthogonalise and muon_step).
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes, ndim: int = 2, device=None) -> torch.Tensor:
+    """A CUDA matrix whose rows are contiguous (any row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t
+
+
+def _ld(t: torch.Tensor, multiple: int = 1) -> int:
+    """Row stride in elements (for a single row, its length rounded up to `multiple`)."""
+    return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // multiple) * multiple
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """The call's device and stream: the tensors' device made current, the
+    given stream (or that device's current one) for allocations and launches."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"stream must be on {device}")
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _code_room(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """[rows, cols] codes in rows of a multiple of 16 bytes."""
+    return torch.empty((rows, -(-cols // 16) * 16), dtype=dtype, device=device)[:, :cols]
+
+
+def _scale_room(rows: int, cols: int, block_rows: int, device) -> torch.Tensor:
+    """One scale for each block, in rows of a multiple of 4 bytes."""
+    n = -(-cols // _BLOCK)
+    return torch.empty((-(-rows // block_rows), -(-n // 4) * 4), dtype=torch.float8_e8m0fnu, device=device)[:, :n]
+
+
+def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float8_e4m3fn,
+                 minus: Optional[torch.Tensor] = None, layout: str = "rows", stream=None) -> Tuple[torch.Tensor, ...]:
+    """bcjr_fp8_quantise: 8-bit codes of a matrix ``x`` (fp32, fp16, bf16; ``x - minus``
+    with an fp32 ``minus``) and their power-of-two scales, one for each 128 values of
+    a row (``block_rows`` 1) or for each 128 x 128 block (``block_rows`` 128).
+
+    ``layout`` "rows" returns (codes [rows, cols], scales [ceil(rows / block_rows),
+    ceil(cols / 128)] float8_e8m0fnu); "cols" the same of the transpose of x
+    (codes [cols, rows], blocks down the columns of x); "both" all four, from one
+    pass over x.  The rows of the codes start at multiples of 16 bytes, as
+    fp8_matmul takes them."""
+    _matrix(x, "x", _WIDE)
+    if block_rows not in (1, _BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    if dtype not in _CODES:
+        raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+    if layout not in ("rows", "cols", "both"):
+        raise ValueError('layout must be "rows", "cols" or "both"')
+    if minus is not None:
+        _matrix(minus, "minus", (torch.float32,), device=x.device)
+        if minus.shape != x.shape:
+            raise ValueError("minus must have the shape of x")
+    rows, cols = x.shape
+    with _on(x.device, stream) as st:
+        q = s = qt = s_t = None
+        if layout != "cols":
+            q, s = _code_room(rows, cols, dtype, x.device), _scale_room(rows, cols, block_rows, x.device)
+        if layout != "rows":
+            qt, s_t = _code_room(cols, rows, dtype, x.device), _scale_room(cols, rows, block_rows, x.device)
+        rc = load().bcjr_fp8_quantise(
+            _ptr(x), _TYPES[x.dtype], rows, cols, _ld(x), _ptr(minus), 0 if minus is None else _ld(minus),
+            _TYPES[dtype], block_rows, _ptr(q), 0 if q is None else q.stride(0), _ptr(s), 0 if s is None else s.stride(0),
+            _ptr(qt), 0 if qt is None else qt.stride(0), _ptr(s_t), 0 if s_t is None else s_t.stride(0), st)
+    _check(rc, "bcjr_fp8_quantise")
+    return (q, s) if layout == "rows" else (qt, s_t) if layout == "cols" else (q, s, qt, s_t)
+
+
+def _scaled(q: torch.Tensor, scale: torch.Tensor, name: str, device) -> int:
+    """Checks codes and their scales; returns the rows that share a scale."""
+    _matrix(q, name, _CODES, device=device)
+    _matrix(scale, f"scale_{name}", (torch.float8_e8m0fnu,), device=device)
+    if q.numel() and ((q.shape[0] > 1 and q.stride(0) % 16 != 0) or q.data_ptr() % 16 != 0):
+        raise ValueError(f"the rows of {name} must start at multiples of 16 bytes")
+    blocks = -(-q.shape[1] // _BLOCK)
+    for rows in (1, _BLOCK):
+        if tuple(scale.shape) == (-(-q.shape[0] // rows), blocks):
+            return rows
+    raise ValueError(f"scale_{name} must be [{q.shape[0]}, {blocks}] or [{-(-q.shape[0] // _BLOCK)}, {blocks}]")
+
+
+def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor, alpha: float = 1.0,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """bcjr_fp8_matmul: alpha (a scale_a) (b scale_b)^T, [M, N], from 8-bit codes a [M, K]
+    and b [N, K] (e4m3 or e5m2 each) with one scale for each 128 values of K and
+    each row or 128 rows, as fp8_quantise gives them.  Sums are in fp32, the
+    result (fp32, fp16 or bf16; ``out``, if given, with any row stride) is rounded once."""
+    a_rows = _scaled(a, scale_a, "a", None)
+    b_rows = _scaled(b, scale_b, "b", a.device)
+    (M, K), (N, Kb) = a.shape, b.shape
+    if K != Kb:
+        raise ValueError("a and b must have the same number of columns")
+    if out is None:
+        if out_dtype not in _WIDE:
+            raise TypeError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    else:
+        _matrix(out, "out", _WIDE, device=a.device)
+        if tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be [{M}, {N}]")
+    with _on(a.device, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        rc = load().bcjr_fp8_matmul(
+            _ptr(a), _TYPES[a.dtype], _ld(a, 16), _ptr(scale_a), _ld(scale_a), a_rows, _ptr(b), _TYPES[b.dtype],
+            _ld(b, 16), _ptr(scale_b), _ld(scale_b), b_rows, M, N, K, float(alpha), _ptr(out), _TYPES[out.dtype],
+            _ld(out), st)
+    _check(rc, "bcjr_fp8_matmul")
+    return out
+
+
+def _coeffs(coeffs, steps: int):
+    """(a, b, c) for every step, or one triple for each, as a C array; None for the default."""
+    if coeffs is None:
+        return None
+    flat = [float(v) for t in coeffs for v in (t if isinstance(t, (tuple, list)) else (t,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("coeffs must be (a, b, c) or one (a, b, c) for each step")
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = None, eps: float = 1e-7,
+                  out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """bcjr_orthogonalise: Newton-Schulz orthogonalisation of a matrix or a batch of
+    matrices ``g`` ([rows, cols] or [batch, rows, cols]; fp32, fp16, bf16) after
+    division by its Frobenius norm + eps; fp16 or bf16 of the shape of g.  Products
+    take fp16 operands and sum in fp32.  ``coeffs`` is (a, b, c), or one such triple
+    for each step; the default is Muon's."""
+    if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
+        raise ValueError("g must be a matrix or a batch of matrices")
+    _matrix(g, "g", _WIDE, ndim=g.dim())
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float16")
+    rows, cols = g.shape[-2:]
+    batch = g.shape[0] if g.dim() == 3 else 1
+    co = _coeffs(coeffs, steps)
+    with _on(g.device, stream) as st:
+        out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
+        rc = load().bcjr_orthogonalise(_ptr(g), _TYPES[g.dtype], batch, rows, cols, _ld(g),
+                                       g.stride(0) if g.dim() == 3 else 0, int(steps), co, float(eps), _ptr(out),
+                                       _TYPES[out_dtype], cols, rows * cols, st)
+    _check(rc, "bcjr_orthogonalise")
+    return out
+
+
+def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: float, mu: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, scale: Optional[float] = None, steps: int = 5,
+              coeffs: Optional[Sequence] = None, eps: float = 1e-7, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """bcjr_muon_step: one Muon step on a weight matrix; updates ``w`` and ``momentum``
+    (fp32) in place from ``grad`` (fp32, fp16, bf16) and returns them:
+    momentum = mu momentum + grad; u = grad + mu momentum (or momentum without
+    nesterov); w = (1 - lr weight_decay) w - lr scale orthogonalise(u).
+    ``scale`` defaults to sqrt(max(1, rows / cols))."""
+    _matrix(w, "w", (torch.float32,))
+    _matrix(grad, "grad", _WIDE, device=w.device)
+    _matrix(momentum, "momentum", (torch.float32,), device=w.device)
+    if grad.shape != w.shape or momentum.shape != w.shape:
+        raise ValueError("grad and momentum must have the shape of w")
+    rows, cols = w.shape
+    if scale is None:
+        scale = math.sqrt(max(1.0, rows / cols)) if cols else 1.0
+    co = _coeffs(coeffs, steps)
+    with _on(w.device, stream) as st:
+        rc = load().bcjr_muon_step(_ptr(w), _ld(w), _ptr(grad), _TYPES[grad.dtype], _ld(grad), _ptr(momentum),
+                                   _ld(momentum), rows, cols, float(lr), float(mu), int(bool(nesterov)),
+                                   float(weight_decay), float(scale), int(steps), co, float(eps), st)
+    _check(rc, "bcjr_muon_step")
+    return w, momentum

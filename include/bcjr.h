@@ -196,13 +196,113 @@ BCJR_API int bcjr_qat_step(float* w, const float* w_target, int64_t n_seq, int64
                            float* grad_w, float* grad_codebook, void* stream);
 
 /*
+ * Layer-wise quantisation-aware training.
+ *
+ * The loss of a layer is the change of its outputs, ||X (W_hat - W*)^T||^2 for
+ * activations X ("Experimental Results": per-layer reconstruction MSE).  Its
+ * products run on 8-bit operands (bcjr_fp8_quantise, bcjr_fp8_matmul), its
+ * gradient goes through bcjr_vjp to the latent weights, and bcjr_muon_step
+ * updates them as matrices (bcjr_orthogonalise is its orthogonalisation alone).
+ *
+ * Matrices are row-major with a row stride `ld` in elements, at least the
+ * number of columns; what lies behind a row's columns is neither read nor
+ * written.  Every pointer must belong to the current device (or be managed)
+ * and be aligned to its element type, 8-bit codes to 16 bytes with a row stride
+ * that is a multiple of 16; otherwise BCJR_ERR_INVALID_ARG.  Outputs must not
+ * overlap inputs or one another, except that a weight, momentum or gradient
+ * updated in place is itself.  Calls may be captured into a CUDA graph.
+ */
+typedef enum {
+  BCJR_F32 = 0,
+  BCJR_F16 = 1,
+  BCJR_BF16 = 2,
+  BCJR_E4M3 = 3,   /* 8-bit: 4 exponent bits, largest value 448, no infinities */
+  BCJR_E5M2 = 4    /* 8-bit: 5 exponent bits, largest value 57344 */
+} bcjr_dtype;
+
+/*
+ * 8-bit codes with one power-of-two scale for each block of 128 values of a
+ * row (block_rows = 1) or of 128 rows x 128 columns (block_rows = 128).  With
+ * v = x, or x - minus in fp32, and FMAX = 448 or 57344,
+ *   scale = 2^e, e the least integer >= -127 with max |v| <= FMAX 2^e over the
+ *           block (e = 0 for a block of zeros),
+ *   q     = v / scale rounded to the nearest 8-bit value, ties to even,
+ * so that q * scale stands for v.  The scale is stored as the byte e + 127 (the
+ * E8M0 type).  A block that holds a NaN or an infinity gets the scale NaN (255)
+ * and NaN codes.  The codes of v^T (blocks of 128 values of its rows, i.e. down
+ * the columns of x) come from the same pass over x.
+ *   x       [rows][cols]  fp32, fp16 or bf16 (input)
+ *   minus   [rows][cols]  fp32, or NULL (input)
+ *   q       [rows][cols], scale   [ceil(rows / block_rows)][ceil(cols / 128)]
+ *   qt      [cols][rows], scale_t [ceil(cols / block_rows)][ceil(rows / 128)]
+ * q and scale, or qt and scale_t, may be NULL (not both pairs).  rows or cols
+ * of 0 is a no-op.
+ */
+BCJR_API int bcjr_fp8_quantise(const void* x, int x_type, int64_t rows, int64_t cols, int64_t ld_x,
+                               const float* minus, int64_t ld_minus, int q_type, int block_rows, void* q,
+                               int64_t ld_q, void* scale, int64_t ld_scale, void* qt, int64_t ld_qt,
+                               void* scale_t, int64_t ld_scale_t, void* stream);
+
+/*
+ * Product of two matrices of 8-bit codes with block scales, summed in fp32:
+ *   out[m][n] = alpha sum_k (a[m][k] scale_a[m / a_block_rows][k / 128])
+ *                         * (b[n][k] scale_b[n / b_block_rows][k / 128]).
+ * With the codes of activations X and weights W that is X W^T; with those of W
+ * transposed it is the gradient dY W, with those of dY and X transposed the
+ * gradient dY^T X.
+ *   a    [M][K], b [N][K]  e4m3 or e5m2, each of its own type (input)
+ *   out  [M][N]            fp32, fp16 or bf16 (output), rounded once
+ * M or N of 0 is a no-op, K of 0 gives zeros.  A NaN code or scale makes the
+ * entries of out that it enters NaN.  Results are the same bits run to run.
+ */
+BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void* scale_a, int64_t ld_scale_a,
+                             int a_block_rows, const void* b, int b_type, int64_t ld_b, const void* scale_b,
+                             int64_t ld_scale_b, int b_block_rows, int64_t M, int64_t N, int64_t K, float alpha,
+                             void* out, int out_type, int64_t ld_out, void* stream);
+
+/*
+ * Orthogonalisation of an update by Newton-Schulz products (as in Muon): with
+ * X_0 = G / (||G||_F + eps) and, for each of `steps` steps and its coefficients
+ * (a, b, c), X <- a X + (b A + c A^2) X where A = X X^T (X^T X from the right
+ * when rows > cols), out is the last X: G with its singular values moved
+ * towards 1.  Iterates and Gram matrices are held in fp16 scaled by 2^12
+ * (11 bits of mantissa; products summed in fp32), so out, fp16 or bf16, is
+ * within about 1e-3 of the exact iteration in the 2-norm.
+ *   g       [batch][rows][cols]  fp32, fp16 or bf16 (input)
+ *   coeffs  [steps][3]           HOST pointer, read during the call, or NULL
+ *                                for Muon's (3.4445, -4.7750, 2.0315)
+ *   out     [batch][rows][cols]  fp16 or bf16 (output)
+ * rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.  Coefficients that drive a
+ * singular value of [0, 1] above 2 are BCJR_ERR_INVALID_ARG.  A matrix of zeros
+ * gives zeros (eps > 0); NaN or infinities make that matrix NaN.
+ */
+BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g,
+                                int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out,
+                                int out_type, int64_t ld_out, int64_t batch_stride_out, void* stream);
+
+/*
+ * One Muon step on a matrix of latent weights, all in place:
+ *   momentum <- mu momentum + grad
+ *   u         = grad + mu momentum (nesterov != 0), or momentum
+ *   w        <- (1 - lr weight_decay) w - lr scale orthogonalise(u)
+ *   w, momentum  [rows][cols] fp32 (updated), grad [rows][cols] fp32, fp16 or bf16
+ * steps, coeffs and eps as in bcjr_orthogonalise; lr, mu, weight_decay and scale
+ * finite.
+ */
+BCJR_API int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad,
+                            float* momentum, int64_t ld_momentum, int64_t rows, int64_t cols, float lr, float mu,
+                            int nesterov, float weight_decay, float scale, int steps, const float* coeffs,
+                            float eps, void* stream);
+
+/*
  * Synchronises `stream` and returns BCJR_OK, or BCJR_ERR_CUDA if the stream
  * holds a CUDA error, or the first device-side error recorded by a kernel of
  * this library since the last call (BCJR_ERR_NUMERIC: a step's posterior mass
  * left 1 +- 1e-2 or was not finite; BCJR_ERR_TIMEOUT: a wait of the L=16 V=1
  * VJP for a bulk copy into its shared-memory codeword ring did not end within
  * 1 s, after which that CTA computes on without the ring and its sequences'
- * outputs are not usable).  The flag is one per device and process, shared by
+ * outputs are not usable; or a wait of a matrix product for its copies or sums,
+ * after which that tile is not written).  The flag is one per device and process, shared by
  * all streams; reading it clears it.
  */
 BCJR_API int bcjr_get_device_error(void* stream);
