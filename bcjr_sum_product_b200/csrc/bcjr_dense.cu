@@ -2,6 +2,7 @@
 // block quantisation, the block-scaled product, Newton-Schulz orthogonalisation
 // and the Muon step.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -111,36 +112,77 @@ int make_map(CUtensorMap* map, const Operand& o, int elem, int box) {
   return r == CUDA_SUCCESS ? BCJR_OK : BCJR_ERR_CUDA;
 }
 
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
-int launch_tile(const Operand& r, const Operand& c, G::Params p, int64_t tiles, int64_t batch, cudaStream_t st) {
-  using S = G::Shape<KIND, BN>;
-  constexpr int elem = KIND == G::MX ? 1 : 2;
-  CUtensorMap mr, mc;
-  if (int rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) return rc;
-  if (int rc = make_map(&mc, c, elem, C_MN ? 64 : BN)) return rc;
-  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
+// cudaFuncSetAttribute once for each kernel and device.
+int allow_smem(const void* kern, std::atomic<uint64_t>* done, int smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return BCJR_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_relaxed) & bit)) return BCJR_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
+  if (dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
+  return BCJR_OK;
+}
+
+// `chained`: the call's own earlier kernel precedes this one on the stream, whose
+// set-up may then overlap that one's end (both kernels wait for it before they touch
+// its results).
+template <class Kern>
+int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cluster, bool chained, const CUtensorMap& mr,
+           const CUtensorMap& mc, const G::Params& p, cudaStream_t st) {
+  if (grid > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.splits;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.splits), 1, (unsigned)batch);
-  cfg.blockDim = dim3(G::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.gridDim = dim3((unsigned)grid, 1, (unsigned)batch);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = chained ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, mr, mc, p) != cudaSuccess) {
     cudaGetLastError();
     return BCJR_ERR_CUDA;
   }
   counted_launch();
   return BCJR_OK;
+}
+
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+int launch_tile(const Operand& r, const Operand& c, const G::Params& p, bool chained, cudaStream_t st) {
+  using S = G::TileShape<KIND, BN>;
+  constexpr int elem = KIND == G::MX ? 1 : 2;
+  static std::atomic<uint64_t> done{0};
+  CUtensorMap mr, mc;
+  int rc;
+  if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN))) return rc;
+  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI>;
+  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
+  return launch(kern, (int64_t)p.tiles * p.splits, p.batch, G::kTileThreads, S::kSmem, p.splits, chained, mr, mc, p, st);
+}
+
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm, bool chained, cudaStream_t st) {
+  using S = G::PairShape<KIND, BN>;
+  constexpr int elem = KIND == G::MX ? 1 : 2;
+  static std::atomic<uint64_t> done{0};
+  CUtensorMap mr, mc;
+  int rc;
+  if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN / 2))) return rc;
+  auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI>;
+  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
+  const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
+  return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, chained, mr, mc, p, st);
 }
 
 // Blocks of one tile: as many (1, 2, 4 or 8) as the tiles leave room for, each with at least two stages of k.
@@ -153,31 +195,42 @@ int splits_for(int64_t tiles, int64_t stages, int nsm) {
 // ------------------------------------------------------------ 8-bit product
 
 template <int BN>
-int matmul_bn(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
+int matmul_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   const int64_t tiles = parts(p.rows, G::kRowsTile) * parts(p.cols, BN);
   if (tiles * 8 > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
+  p.tiles = (int)tiles;
   p.splits = splits_for(tiles, parts(p.k, 128), nsm);
-  return launch_tile<G::MX, BN, false, false, G::OUT>(r, c, p, tiles, 1, st);
+  return launch_tile<G::MX, BN, false, false, G::OUT>(r, c, p, false, st);
+}
+template <int BN>
+int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
+  const int64_t tiles = parts(p.rows, 2 * G::kRowsTile) * parts(p.cols, BN);
+  if (tiles > INT32_MAX / 2) return BCJR_ERR_UNSUPPORTED;
+  p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
+  p.tiles = (int)tiles;
+  return launch_pair<G::MX, BN, false, false, G::OUT>(r, c, p, nsm, false, st);
 }
 
-int run_matmul(const Operand& r, const Operand& c, const G::Params& p, cudaStream_t st) {
+int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
   int nsm = 0;
   if (int rc = sm_count(&nsm)) return rc;
-  if (p.cols <= 16) return matmul_bn<16>(r, c, p, nsm, st);
-  if (p.cols <= 32) return matmul_bn<32>(r, c, p, nsm, st);
-  if (p.cols <= 64) return matmul_bn<64>(r, c, p, nsm, st);
-  if (p.cols <= 128 || parts(p.rows, 128) * parts(p.cols, 256) < nsm) return matmul_bn<128>(r, c, p, nsm, st);
-  return matmul_bn<256>(r, c, p, nsm, st);
+  p.batch = 1;
+  if (p.cols <= 16) return matmul_tile<16>(r, c, p, nsm, st);
+  if (p.cols <= 32) return matmul_tile<32>(r, c, p, nsm, st);
+  if (p.cols <= 64) return matmul_tile<64>(r, c, p, nsm, st);
+  if (parts(p.rows, 256) * parts(p.cols, 224) * 4 >= nsm) return matmul_pair<224>(r, c, p, nsm, st);
+  return matmul_tile<128>(r, c, p, nsm, st);
 }
 
 // ------------------------------------------------------------ Newton-Schulz
 
 constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// The iterates are kept in fp16 with headroom for entries up to 16; the singular
-// values of u / |u| lie in [0, 1].  False if the coefficients drive a singular
-// value (sampled over the interval that each step can reach) above 2.
+// The iterates and polynomials are kept in fp16 with headroom for entries up to
+// 16; the singular values of u / |u| lie in [0, 1].  False if, sampled over the
+// interval that each step can reach, the coefficients drive a singular value
+// above 2 or a + b t + c t^2 above 8.
 bool coeffs_bounded(const float* co, int steps) {
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
@@ -186,7 +239,7 @@ bool coeffs_bounded(const float* co, int steps) {
     for (int i = 0; i <= 256; ++i) {
       const double x = top * i / 256.0, t = x * x;
       most = std::max(most, std::fabs(x * (a + t * (b + t * c))));
-      inner = std::max(inner, std::fabs(t * (b + t * c)));
+      inner = std::max(inner, std::fabs(a + t * (b + t * c)));
     }
     if (!(most <= 2.0) || !(inner <= 8.0)) return false;
     top = most;
@@ -206,39 +259,54 @@ int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps)
   return BCJR_OK;
 }
 
+// P = X X^T (or X^T X), B = a I + b P + c P^2: x against itself, tiles up to the diagonal.
 template <int BN, int EPI, bool MN>
-int sym_bn(const Operand& x, G::Params p, int64_t batch, int nsm, cudaStream_t st) {
-  const int64_t t = parts(p.rows, 128), tiles = (128 / BN) * t * (t + 1) / 2;
-  p.tiles_r = (int)t;
-  p.splits = splits_for(tiles * batch, parts(p.k, 64), nsm);
-  return launch_tile<G::F16, BN, MN, MN, EPI>(x, x, p, tiles, batch, st);
+int sym_tile(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, G::kRowsTile);
+  p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64), nsm);
+  return launch_tile<G::F16, BN, MN, MN, EPI>(x, x, p, true, st);
+}
+template <int BN, int EPI, bool MN>
+int sym_pair(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, 2 * G::kRowsTile);
+  p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
+  return launch_pair<G::F16, BN, MN, MN, EPI>(x, x, p, nsm, true, st);
 }
 template <int EPI, bool MN>
-int run_sym(const Operand& x, const G::Params& p, int64_t batch, int nsm, cudaStream_t st) {
-  const int64_t t = parts(p.rows, 128);
-  if (t * (t + 1) / 2 * batch * 2 < nsm) return sym_bn<64, EPI, MN>(x, p, batch, nsm, st);
-  return sym_bn<128, EPI, MN>(x, p, batch, nsm, st);
+int run_sym(const Operand& x, const G::Params& p, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
+  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN>(x, p, nsm, st);
+  if (t * (t + 1) / 2 * p.batch * 2 < nsm) return sym_tile<64, EPI, MN>(x, p, nsm, st);
+  return sym_tile<128, EPI, MN>(x, p, nsm, st);
 }
 
+// X' = B X (or X B).
 template <int BN, int EPI, bool R_MN>
-int iter_bn(const Operand& r, const Operand& c, G::Params p, int64_t batch, int nsm, cudaStream_t st) {
-  p.tiles_r = (int)parts(p.rows, 128);
-  const int64_t tiles = p.tiles_r * parts(p.cols, BN);
-  p.splits = splits_for(tiles * batch, parts(p.k, 64), nsm);
-  return launch_tile<G::F16, BN, R_MN, false, EPI>(r, c, p, tiles, batch, st);
+int iter_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
+  p.tiles_r = (int)parts(p.rows, G::kRowsTile);
+  p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64), nsm);
+  return launch_tile<G::F16, BN, R_MN, false, EPI>(r, c, p, true, st);
+}
+template <int BN, int EPI, bool R_MN>
+int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
+  p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
+  p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
+  return launch_pair<G::F16, BN, R_MN, false, EPI>(r, c, p, nsm, true, st);
 }
 template <int EPI, bool R_MN>
-int run_iter(const Operand& r, const Operand& c, const G::Params& p, int64_t batch, int nsm, cudaStream_t st) {
-  const int64_t t = parts(p.rows, 128);
-  if (p.cols <= 64 || t * parts(p.cols, 128) * batch * 2 < nsm) return iter_bn<64, EPI, R_MN>(r, c, p, batch, nsm, st);
-  if (p.cols <= 128 || t * parts(p.cols, 256) * batch < nsm) return iter_bn<128, EPI, R_MN>(r, c, p, batch, nsm, st);
-  return iter_bn<256, EPI, R_MN>(r, c, p, batch, nsm, st);
+int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
+  const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
+  if (t2 * parts(p.cols, 256) * p.batch * 4 >= nsm) return iter_pair<256, EPI, R_MN>(r, c, p, nsm, st);
+  if (p.cols <= 64 || t * parts(p.cols, 128) * p.batch * 2 < nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
+  return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
 }
 
 template <int T>
 void launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
-  Q::norm_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), 256, 0, st>>>(u);
-  Q::start_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), 256, 0, st>>>(u);
+  Q::norm_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), Q::kUpdateThreads, 0, st>>>(u);
+  Q::start_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), Q::kUpdateThreads, 0, st>>>(u);
   counted_launch(2);
 }
 
@@ -252,7 +320,9 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   const int64_t m = std::min(sh.rows, sh.cols);
   const int64_t ld_x = up(sh.cols, 8), ld_p = up(m, 8);
   const int64_t nx = sh.rows * ld_x, np = m * ld_p;
-  u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(sh.rows * sh.cols, 1024), parts(4 * nsm, sh.batch)));
+  // warps take 512 columns of a row at a time; enough blocks of eight warps for every SM four times over
+  const int64_t items = sh.rows * parts(sh.cols, Q::kSpan);
+  u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
   __half *x0, *x1, *pp, *bb;
   double* partial;
   auto layout = [&](Arena& ar) {
@@ -277,6 +347,9 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   u.rows = (int)sh.rows;
   u.cols = (int)sh.cols;
   u.scale = G::kIterScale;
+  u.vec = u.ld_g % 4 == 0 && (sh.batch == 1 || u.batch_g % 4 == 0) &&
+          reinterpret_cast<uintptr_t>(u.g) % (4 * size_of(g_type)) == 0 &&
+          (u.momentum == nullptr || (u.ld_m % 4 == 0 && reinterpret_cast<uintptr_t>(u.momentum) % 16 == 0));
   if (g_type == BCJR_F32) launch_update<Q::IN_F32>(u, sh.batch, st);
   else if (g_type == BCJR_F16) launch_update<Q::IN_F16>(u, sh.batch, st);
   else launch_update<Q::IN_BF16>(u, sh.batch, st);
@@ -290,10 +363,11 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     G::Params p{};
     p.rows = p.cols = (int)m;
     p.k = (int)(tall ? sh.rows : sh.cols);
+    p.batch = (int)sh.batch;
     p.out = pp;
     p.ld_out = ld_p;
     p.batch_out = np;
-    rc = tall ? run_sym<G::GRAM, true>(x, p, sh.batch, nsm, st) : run_sym<G::GRAM, false>(x, p, sh.batch, nsm, st);
+    rc = tall ? run_sym<G::GRAM, true>(x, p, nsm, st) : run_sym<G::GRAM, false>(x, p, nsm, st);
     if (rc) break;
     const Operand gram{pp, m, m, ld_p, sh.batch, np};
     p.k = (int)m;
@@ -301,9 +375,10 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     p.x = pp;
     p.ld_x = ld_p;
     p.batch_x = np;
-    p.fa = co[2];
+    p.fa = co[0];
     p.fb = co[1];
-    if ((rc = run_sym<G::POLY, false>(gram, p, sh.batch, nsm, st))) break;
+    p.fc = co[2];
+    if ((rc = run_sym<G::POLY, false>(gram, p, nsm, st))) break;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
     const Operand poly{bb, m, m, ld_p, sh.batch, np};
     const bool end = s + 1 == steps;
@@ -311,18 +386,13 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     q.rows = (int)sh.cols;
     q.cols = (int)sh.rows;
     q.k = (int)m;
-    q.x = x0;
-    q.ld_x = ld_x;
-    q.batch_x = nx;
-    q.fa = 1.f;
-    q.fb = co[0];
+    q.batch = (int)sh.batch;
     if (!end) {
       q.out = x1;
       q.ld_out = ld_x;
       q.batch_out = nx;
     }
-#define BCJR_ITER(E) \
-  (tall ? run_iter<E, false>(poly, x, q, sh.batch, nsm, st) : run_iter<E, true>(x, poly, q, sh.batch, nsm, st))
+#define BCJR_ITER(E) (tall ? run_iter<E, false>(poly, x, q, nsm, st) : run_iter<E, true>(x, poly, q, nsm, st))
     rc = !end ? BCJR_ITER(G::ITER) : epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
 #undef BCJR_ITER
     std::swap(x0, x1);

@@ -2,7 +2,7 @@
 //
 //   D[r][c] = sum_k R[r][k] C[c][k]
 //
-// R is the side of 128 tensor-memory lanes, C the side of its columns.  Every
+// R is the side of the tensor-memory lanes, C the side of its columns.  Every
 // result is stored row-major with r along the row, so that the 32 lanes of a
 // warp write neighbouring values: the product y = a b^T takes R = b, C = a.
 //
@@ -17,13 +17,13 @@
 //        over all of k stays in tensor memory in fp32 and nothing is rescaled
 //        outside it.
 //
-// One block computes one 128 x BN tile over its share of k.  Warp 0 fills a
-// ring of shared-memory stages by TMA (128 bytes of k each, 128-byte swizzle),
-// one thread of warp 1 issues the products, warps 2 to 5 bring the scales (MX)
-// and then read the sums.  Where there are too few tiles for the GPU's 148
-// SMs, a cluster of blocks splits k: each leaves its sums in shared memory and
-// adds up its share of the columns over the cluster, in the order of the
-// ranks, so the result does not depend on timing.
+// Two kernels:
+//   tile_kernel  one block, one 128 x BN tile, with k split over a cluster
+//                where there are few tiles: for small products;
+//   pair_kernel  persistent pairs of blocks, 256 x BN tiles, sums of one tile
+//                read out while the next is computed: for large ones.
+// Both fill a ring of shared-memory stages by TMA (128 bytes of k each,
+// 128-byte swizzle) from one thread and issue the products from another.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,10 +41,10 @@ enum Kind { F16 = 0, MX = 1 };
 enum Epilogue {
   OUT = 0,    // out = alpha D
   GRAM = 1,   // P = D, symmetric, both halves stored
-  POLY = 2,   // B = b P + c D, symmetric, both halves stored
-  ITER = 3,   // X' = a X + D
-  LAST = 4,   // out = a X + D
-  STEP = 5    // w = keep w - rate (a X + D)
+  POLY = 2,   // B = a I + b P + c D, symmetric, both halves stored
+  ITER = 3,   // X' = D
+  LAST = 4,   // out = D
+  STEP = 5    // w = keep w - rate D
 };
 enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 
@@ -56,7 +56,9 @@ constexpr float kIterScale = 4096.f;
 struct Params {
   int rows, cols, k;         // extents of r, c, k
   int tiles_r;               // tiles along r
-  int splits;                // blocks of one tile (the cluster)
+  int tiles;                 // tiles of one matrix
+  int batch;
+  int splits;                // blocks of one tile (the cluster of tile_kernel)
   // MX
   const uint8_t* sr;         // scales of R: sr[(r >> shift_r) * ld_sr + k / 128]
   const uint8_t* sc;
@@ -65,32 +67,16 @@ struct Params {
   int fmt_r, fmt_c;          // 0: e4m3, 1: e5m2
   // epilogue
   void* out;
-  const __half* x;           // P (POLY) or X (ITER, LAST, STEP), laid out as D
+  const __half* x;           // P (POLY), laid out as D
   int64_t ld_out, ld_x;
   int64_t batch_out, batch_x;
   int out_type;
-  float fa, fb;              // OUT: alpha; POLY: c and b; ITER, LAST, STEP: 1 and a
+  float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
 };
 
-constexpr int kThreads = 192;
-constexpr int kRowsTile = 128;
+constexpr int kRowsTile = 128;                      // rows of a block's tile
 constexpr int kStageBytesR = kRowsTile * 128;
-
-template <int KIND, int BN>
-struct Shape {
-  static constexpr int kStageBytes = kStageBytesR + BN * 128;
-  // as many stages as fit beside one another: two blocks on an SM up to 128 columns
-  static constexpr int kStages = BN <= 128 ? (BN <= 64 ? 4 : 3) : 4;
-  static constexpr int kScaleStages = 2;                       // MX: rings of 512 values of k
-  static constexpr int kScaleBytes = KIND == MX ? 512 + 512 * ((BN + 127) / 128) : 0;
-  static constexpr int kScaleCols = KIND == MX ? 4 + 4 * ((BN + 127) / 128) : 0;
-  static constexpr int kUsedCols = BN + kScaleStages * kScaleCols;
-  static constexpr int kTmemCols = kUsedCols <= 32 ? 32 : kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
-  static constexpr int kDumpBytes = kRowsTile * BN * 4;        // sums left for the cluster, over the stages
-  static constexpr int kRing = kStages * kStageBytes > kDumpBytes ? kStages * kStageBytes : kDumpBytes;
-  static constexpr int kSmem = 1024 + kRing + kScaleStages * kScaleBytes + 256;
-};
 
 template <int T>
 __device__ __forceinline__ void store_one(void* out, int64_t i, float v) {
@@ -98,46 +84,68 @@ __device__ __forceinline__ void store_one(void* out, int64_t i, float v) {
   else if (T == OUT_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
 }
-
-// Stores 16 columns c0..c0+15 of row r (of which `n` exist).
-template <int EPI>
-__device__ __forceinline__ void finish16(const Params& p, int64_t batch, int r, int c0, int n, bool mirror,
-                                         const float (&v)[16]) {
-  if (r >= p.rows) return;
-  if (EPI == OUT) {
-    const int64_t at = (int64_t)c0 * p.ld_out + r;
-#define BCJR_STORE(T)                                                                      \
-  _Pragma("unroll") for (int i = 0; i < 16; ++i) if (i < n)                                \
-      store_one<T>(p.out, at + (int64_t)i * p.ld_out, p.fa * v[i]);
-    if (p.out_type == OUT_F32) { BCJR_STORE(OUT_F32) }
-    else if (p.out_type == OUT_F16) { BCJR_STORE(OUT_F16) }
-    else { BCJR_STORE(OUT_BF16) }
-#undef BCJR_STORE
-    return;
-  }
-  float y[16];
-  if (EPI == GRAM) {
+template <int T>
+__device__ __forceinline__ void store16(void* out, int64_t at, int64_t ld, int n, const float (&v)[16]) {
+  if (n >= 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = v[i] * (1.f / kIterScale);
+    for (int i = 0; i < 16; ++i) store_one<T>(out, at + (int64_t)i * ld, v[i]);
   } else {
-    const __half* x = p.x + batch * p.batch_x + (int64_t)c0 * p.ld_x + r;
-    float xv[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) xv[i] = i < n ? __half2float(x[(int64_t)i * p.ld_x]) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = fmaf(p.fb, xv[i], p.fa * (1.f / kIterScale) * v[i]);
-  }
-  if (EPI == GRAM || EPI == POLY || EPI == ITER) {
-    __half h[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = __float2half_rn(y[i]);
-    __half* o = static_cast<__half*>(p.out) + batch * p.batch_out;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < n) o[(int64_t)(c0 + i) * p.ld_out + r] = h[i];
+      if (i < n) store_one<T>(out, at + (int64_t)i * ld, v[i]);
+  }
+}
+__device__ __forceinline__ void store16_as(int type, void* out, int64_t at, int64_t ld, int n, const float (&v)[16]) {
+  if (type == OUT_F32) store16<OUT_F32>(out, at, ld, n, v);
+  else if (type == OUT_F16) store16<OUT_F16>(out, at, ld, n, v);
+  else store16<OUT_BF16>(out, at, ld, n, v);
+}
+
+// What the epilogue of columns c0..c0+15 of row r reads, loaded ahead: 16 entries
+// of row r of P (symmetric, so they lie side by side; ld_x is a multiple of 8).
+struct Ahead {
+  uint4 h[2];
+};
+template <int EPI>
+__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead& a) {
+  if (EPI == POLY && r < p.rows) {
+    const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x + c0;
+    a.h[0] = c0 < p.cols ? *reinterpret_cast<const uint4*>(x) : make_uint4(0, 0, 0, 0);
+    a.h[1] = c0 + 8 < p.cols ? *reinterpret_cast<const uint4*>(x + 8) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Stores columns c0..c0+15 (as far as they exist) of row r.
+template <int EPI>
+__device__ __forceinline__ void finish16(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead& a,
+                                         float (&v)[16]) {
+  if (r >= p.rows) return;
+  const int n = p.cols - c0;
+  const int64_t at = batch * p.batch_out + (int64_t)c0 * p.ld_out + r;
+  const float unit = EPI == OUT ? p.fa : EPI == LAST ? 1.f / (kIterScale * kIterScale) : 1.f / kIterScale;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= unit;
+  if constexpr (EPI == OUT || EPI == LAST) {
+    store16_as(p.out_type, p.out, at, p.ld_out, n, v);
+  } else if constexpr (EPI == GRAM || EPI == POLY || EPI == ITER) {
+    if constexpr (EPI == POLY) {
+      const __half* x = reinterpret_cast<const __half*>(a.h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] = fmaf(p.fb, __half2float(x[i]), p.fc * v[i]);
+        if (c0 + i == r) v[i] += p.fa * kIterScale;
+      }
+    }
+    alignas(16) __half h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = __float2half_rn(v[i]);
+    __half* o = static_cast<__half*>(p.out) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) o[(int64_t)i * p.ld_out] = h[i];
     if (EPI != ITER && mirror) {
-      __half* m = o + (int64_t)r * p.ld_out + c0;   // ld_out and c0 are multiples of 8
-      if (n == 16) {
+      __half* m = static_cast<__half*>(p.out) + batch * p.batch_out + (int64_t)r * p.ld_out + c0;   // 16-byte aligned
+      if (n >= 16) {
         reinterpret_cast<uint4*>(m)[0] = reinterpret_cast<const uint4*>(h)[0];
         reinterpret_cast<uint4*>(m)[1] = reinterpret_cast<const uint4*>(h)[1];
       } else {
@@ -146,23 +154,14 @@ __device__ __forceinline__ void finish16(const Params& p, int64_t batch, int r, 
           if (i < n) m[i] = h[i];
       }
     }
-  } else if (EPI == LAST) {
-    const int64_t at = batch * p.batch_out + (int64_t)c0 * p.ld_out + r;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i < n) {
-        if (p.out_type == OUT_F16) store_one<OUT_F16>(p.out, at + (int64_t)i * p.ld_out, y[i] * (1.f / kIterScale));
-        else store_one<OUT_BF16>(p.out, at + (int64_t)i * p.ld_out, y[i] * (1.f / kIterScale));
-      }
-    }
   } else {   // STEP
-    float* w = static_cast<float*>(p.out) + (int64_t)c0 * p.ld_out + r;
+    float* w = static_cast<float*>(p.out) + at;
     float wv[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) wv[i] = i < n ? w[(int64_t)i * p.ld_out] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) w[(int64_t)i * p.ld_out] = fmaf(-p.rate * (1.f / kIterScale), y[i], p.keep * wv[i]);
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(-p.rate * (1.f / kIterScale), v[i], p.keep * wv[i]);
+    store16<OUT_F32>(p.out, at, p.ld_out, n, v);
   }
 }
 
@@ -184,13 +183,66 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int
   return w;
 }
 
+// Tile t of a symmetric product of TR-row and TC-column tiles: row tile j has the
+// (j + 1) TR / TC column tiles up to its diagonal block.
+template <int TR, int TC>
+__device__ __forceinline__ void symmetric_tile(int t, int* tr, int* tc, bool* mirror) {
+  constexpr int q = TR / TC;
+  static_assert(q * TC == TR, "column tiles divide the row tiles");
+  int j = (int)((sqrtf(8.f * (float)(t / q) + 1.f) - 1.f) * 0.5f);
+  while (q * (j + 1) * (j + 2) / 2 <= t) ++j;
+  while (q * j * (j + 1) / 2 > t) --j;
+  *tr = j;
+  *tc = t - q * j * (j + 1) / 2;
+  *mirror = *tc < j * q;
+}
+
+// The products of one stage: four instructions of 32 bytes of k.
+template <int CG, int KIND, bool R_MN, bool C_MN>
+__device__ __forceinline__ void stage_products(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, uint32_t ts, bool add) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 32 bytes along K, or 16 rows of 128 bytes where K runs over the rows
+    const uint64_t da = tc::desc_sw128(a + i * (R_MN ? 2048 : 32), R_MN ? 8192 : 0);
+    const uint64_t db = tc::desc_sw128(b + i * (C_MN ? 2048 : 32), C_MN ? 8192 : 0);
+    if (KIND == MX) tc::mma_mx<CG>(acc, da, db, idesc, ts, ts + 4, add || i > 0);
+    else tc::mma_f16<CG>(acc, da, db, idesc, add || i > 0);
+  }
+}
+
+// ------------------------------------------------------------ small products
+
+constexpr int kTileThreads = 192;
+
+template <int KIND, int BN>
+struct TileShape {
+  static constexpr int kStageBytes = kStageBytesR + BN * 128;
+  static constexpr int kStages = BN <= 64 ? 4 : 3;             // two blocks fit an SM
+  static constexpr int kScaleStages = 2;                       // MX: rings of 512 values of k
+  static constexpr int kScaleBytes = KIND == MX ? 1024 : 0;
+  static constexpr int kScaleCols = KIND == MX ? 8 : 0;
+  static constexpr int kUsedCols = BN + kScaleStages * kScaleCols;
+  static constexpr int kTmemCols = kUsedCols <= 32 ? 32 : kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : 256;
+  static constexpr int kDumpLd = BN + 4;                       // sums left for the cluster, over the stages
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSmem = 1024 + kRing + kScaleStages * kScaleBytes + 256;
+  static_assert(kRowsTile * kDumpLd * 4 <= kRing, "the dump fits the ring");
+};
+
+// One block computes one 128 x BN tile over its share of k.  Warp 0 fills the
+// stages, one thread of warp 1 issues the products, warps 2 to 5 bring the
+// scales (MX) and what the epilogue reads, and then read the sums.  Where there
+// are too few tiles for the GPU's SMs, a cluster of blocks splits k: each leaves
+// its sums in shared memory and adds up its share of the columns over the
+// cluster, in the order of the ranks, so the result does not depend on timing.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
-__global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
-                                                         const __grid_constant__ CUtensorMap map_c, const Params p) {
-  using S = Shape<KIND, BN>;
+__global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
+                                                             const __grid_constant__ CUtensorMap map_c, const Params p) {
+  using S = TileShape<KIND, BN>;
   constexpr bool SYM = EPI == GRAM || EPI == POLY;
   constexpr int kElems = KIND == MX ? 128 : 64;     // values of k in a stage
-  static_assert(!SYM || BN <= 128, "symmetric tiles divide 128");
+  constexpr int kGroups = BN / 16;
+  static_assert(BN <= 128, "");
   static_assert(KIND == F16 || (!R_MN && !C_MN), "8-bit operands are K-major");
   static_assert(!C_MN || BN >= 64, "an MN-major box is 64 wide");
   extern __shared__ uint8_t smem_raw[];
@@ -203,18 +255,13 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
   volatile uint32_t* slot_p = reinterpret_cast<volatile uint32_t*>(smem + (slot - ring));
   volatile int* fail = reinterpret_cast<volatile int*>(smem + (slot + 4 - ring));
 
+  tc::launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x / p.splits, rank = blockIdx.x % p.splits, batch = blockIdx.z;
   int tr, tcn;
   bool mirror = false;
-  if (SYM) {   // row tile j has (j + 1) q column tiles
-    constexpr int q = 128 / (BN < 128 ? BN : 128);
-    int j = (int)((sqrtf(8.f * (float)(tile / q) + 1.f) - 1.f) * 0.5f);
-    while (q * (j + 1) * (j + 2) / 2 <= tile) ++j;
-    while (q * j * (j + 1) / 2 > tile) --j;
-    tr = j;
-    tcn = tile - q * j * (j + 1) / 2;
-    mirror = tcn < j * q;
+  if constexpr (SYM) {
+    symmetric_tile<kRowsTile, BN>(tile, &tr, &tcn, &mirror);
   } else {
     tr = tile % p.tiles_r;
     tcn = tile / p.tiles_r;
@@ -238,16 +285,20 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
     *fail = 0;
     tc::mbar_init_fence();
   }
-  if (warp == 1) tc::tmem_alloc<S::kTmemCols>(slot);
+  if (warp == 1) tc::tmem_alloc<1, S::kTmemCols>(slot);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  tc::wait_for_earlier();
   const uint32_t acc = *slot_p;
   const uint32_t tscale = acc + BN;
   auto gave_up = [&]() {
     *fail = 1;
     atomicCAS(&g_dense_error, 0, kErrTimeout);
   };
+  // the columns whose sums this block finishes: group g of 16 where g % splits == rank
+  Ahead ahead[kGroups];
+  const int row = r0 + 32 * (warp & 3) + lane;      // of warps 2 to 5
 
   if (warp == 0) {
     if (lane == 0) {
@@ -283,43 +334,32 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
     if (lane == 0) {
       const uint32_t idesc = KIND == MX ? tc::idesc_mx(128, BN, p.fmt_r, p.fmt_c) : tc::idesc_f16(128, BN, R_MN, C_MN);
       int it = 0, group = -1, groups = 0;
-      bool add = false, ok = true;
-      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+      uint32_t ts = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const int s = it % S::kStages;
         ok = tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1);
         if (!ok) break;
-        uint32_t ts = 0;
-        if (KIND == MX) {
-          const int ss = (groups - (group == kb / 4 ? 1 : 0)) % S::kScaleStages;
+        if (KIND == MX && group != kb / 4) {
+          group = kb / 4;
+          const int ss = groups % S::kScaleStages;
+          ok = tc::mbar_wait(sfull + 8 * ss, (groups / S::kScaleStages) & 1);
+          if (!ok) break;
+          ++groups;
+          tc::fence_after();
           ts = tscale + ss * S::kScaleCols;
-          if (group != kb / 4) {
-            group = kb / 4;
-            ok = tc::mbar_wait(sfull + 8 * ss, (groups / S::kScaleStages) & 1);
-            if (!ok) break;
-            ++groups;
-            tc::fence_after();
-            const uint32_t src = scales + ss * S::kScaleBytes;
-            tc::copy_scales(ts, tc::desc_scales(src));
-#pragma unroll
-            for (int i = 0; i < (BN + 127) / 128; ++i) tc::copy_scales(ts + 4 + 4 * i, tc::desc_scales(src + 512 + 512 * i));
-          }
+          tc::copy_scales<1>(ts, tc::desc_scales(scales + ss * S::kScaleBytes));
+          tc::copy_scales<1>(ts + 4, tc::desc_scales(scales + ss * S::kScaleBytes + 512));
         }
         tc::fence_after();
-        const uint32_t a = ring + s * S::kStageBytes, b = a + kStageBytesR;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // 32 bytes along K, or 16 rows of 128 bytes where K runs over the rows
-          const uint64_t da = tc::desc_sw128(a + i * (R_MN ? 2048 : 32), R_MN ? 8192 : 0);
-          const uint64_t db = tc::desc_sw128(b + i * (C_MN ? 2048 : 32), C_MN ? 8192 : 0);
-          if (KIND == MX) tc::mma_mx(acc, da, db, tc::idesc_mx_id(idesc, kb & 3), ts, ts + 4, add);
-          else tc::mma_f16(acc, da, db, idesc, add);
-          add = true;
-        }
-        tc::commit(empty + 8 * s);
-        if (KIND == MX && ((kb & 3) == 3 || kb + 1 == kb1)) tc::commit(sempty + 8 * ((groups - 1) % S::kScaleStages));
+        const uint32_t a = ring + s * S::kStageBytes;
+        stage_products<1, KIND, R_MN, C_MN>(acc, a, a + kStageBytesR, KIND == MX ? tc::idesc_mx_id(idesc, kb & 3) : idesc,
+                                            ts, it > 0);
+        tc::commit<1>(empty + 8 * s);
+        if (KIND == MX && ((kb & 3) == 3 || kb + 1 == kb1)) tc::commit<1>(sempty + 8 * ((groups - 1) % S::kScaleStages));
       }
       if (!ok) gave_up();
-      tc::commit(done);
+      tc::commit<1>(done);
     }
   } else {
     const int t = threadIdx.x - 64;   // 0..127
@@ -327,25 +367,22 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
     if (KIND == MX) {
       const int g1 = kb1 > kb0 ? (kb1 - 1) / 4 + 1 : kb0 / 4;
       int n = 0;
-      for (int g = kb0 / 4; g < g1 && ok; ++g, ++n) {
+      for (int g = kb0 / 4; g < g1; ++g, ++n) {
         const int ss = n % S::kScaleStages;
         const uint32_t wr = scale_word(p.sr, p.ld_sr, p.shift_r, r0 + t, p.rows, g, blocks);
-        uint32_t wc[(BN + 127) / 128];
-#pragma unroll
-        for (int i = 0; i < (BN + 127) / 128; ++i) {
-          const int c = 128 * i + t;
-          wc[i] = scale_word(p.sc, p.ld_sc, p.shift_c, c < BN ? c0 + c : p.cols, p.cols, g, blocks);
-        }
+        const uint32_t wc = scale_word(p.sc, p.ld_sc, p.shift_c, t < BN ? c0 + t : p.cols, p.cols, g, blocks);
         ok = tc::mbar_wait(sempty + 8 * ss, ((n / S::kScaleStages) & 1) ^ 1);
         if (!ok) break;
         uint8_t* dst = smem + (scales - ring) + ss * S::kScaleBytes + (t & 31) * 16 + (t >> 5) * 4;
         *reinterpret_cast<uint32_t*>(dst) = wr;
-#pragma unroll
-        for (int i = 0; i < (BN + 127) / 128; ++i) *reinterpret_cast<uint32_t*>(dst + 512 + 512 * i) = wc[i];
+        *reinterpret_cast<uint32_t*>(dst + 512) = wc;
         tc::fence_async_shared();
         tc::mbar_arrive(sfull + 8 * ss);
       }
     }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+      if (g % p.splits == rank) load_ahead<EPI>(p, batch, row, c0 + 16 * g, ahead[g]);
     ok = ok && tc::mbar_wait(done, 0);
     if (!ok) gave_up();
   }
@@ -354,56 +391,64 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
   tc::fence_after();
 
   // The sums: lane r of the warp's quarter, 16 columns at a time.
-  const bool usable = *fail == 0;
+  const bool usable = *fail == 0, some = kb1 > kb0;
+  const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
   if (p.splits == 1) {
     if (warp >= 2 && usable) {
-      const int q = warp & 3, r = r0 + 32 * q + lane;
-      const uint32_t t = acc + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-      for (int j = 0; j < BN; j += 16) {
-        if (c0 + j >= p.cols) break;
+      for (int g = 0; g < kGroups; ++g) {
+        if (c0 + 16 * g >= p.cols) break;
         uint32_t u[16];
         float v[16];
-        if (kb1 > kb0) {
-          tc::tmem_ld16(t + j, u);
+        if (some) {
+          tc::tmem_ld16(sums + 16 * g, u);
           tc::tmem_wait_ld(u);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = kb1 > kb0 ? __uint_as_float(u[i]) : 0.f;
-        finish16<EPI>(p, batch, r, c0 + j, min(16, p.cols - c0 - j), mirror, v);
+        for (int i = 0; i < 16; ++i) v[i] = some ? __uint_as_float(u[i]) : 0.f;
+        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g], v);
       }
     }
   } else {
-    float* dump = reinterpret_cast<float*>(smem);   // [BN][128], over the stages: no copy is in flight
+    float* dump = reinterpret_cast<float*>(smem);   // [128][BN + 4], over the stages: no copy is in flight
+    const int rl = 32 * (warp & 3) + lane;
     if (warp >= 2) {
-      const int q = warp & 3;
-      const uint32_t t = acc + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-      for (int j = 0; j < BN; j += 16) {
+      for (int g = 0; g < kGroups; ++g) {
         uint32_t u[16];
-        if (kb1 > kb0) {
-          tc::tmem_ld16(t + j, u);
+        if (some) {
+          tc::tmem_ld16(sums + 16 * g, u);
           tc::tmem_wait_ld(u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = 0;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dump[(j + i) * 128 + 32 * q + lane] = kb1 > kb0 ? __uint_as_float(u[i]) : 0.f;
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 16 * g + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
       }
     }
     tc::cluster_sync();
     if (warp >= 2 && usable) {
-      const int rl = 32 * (warp & 3) + lane;
-      const int groups = BN / 16;
-      for (int g = rank; g < groups; g += p.splits) {
-        if (c0 + 16 * g >= p.cols) break;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (g % p.splits != rank || c0 + 16 * g >= p.cols) continue;
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
-          const uint32_t src = tc::map_rank(ring, s) + ((16 * g) * 128 + rl) * 4;
+          const uint32_t src = tc::map_rank(ring, s) + (rl * S::kDumpLd + 16 * g) * 4;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += tc::ld_cluster(src + i * 512);
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = tc::ld_cluster4(src + 16 * i);
+            v[4 * i] += f.x;
+            v[4 * i + 1] += f.y;
+            v[4 * i + 2] += f.z;
+            v[4 * i + 3] += f.w;
+          }
         }
-        finish16<EPI>(p, batch, r0 + rl, c0 + 16 * g, min(16, p.cols - c0 - 16 * g), mirror, v);
+        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g], v);
       }
     }
     tc::cluster_sync();
@@ -412,7 +457,267 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const __grid_constant__ 
   __syncthreads();
   if (warp == 1) {
     tc::fence_after();
-    tc::tmem_dealloc<S::kTmemCols>(acc);
+    tc::tmem_dealloc<1, S::kTmemCols>(acc);
+  }
+}
+
+// ------------------------------------------------------------ large products
+
+constexpr int kPairThreads = 256;
+
+template <int KIND, int BN>
+struct PairShape {
+  static constexpr int kStageBytesC = BN / 2 * 128;             // a block brings half of the columns
+  static constexpr int kStageBytes = kStageBytesR + kStageBytesC;
+  static constexpr int kScaleStages = 2;
+  static constexpr int kScaleBytes = KIND == MX ? 512 + 512 * ((BN + 127) / 128) : 0;
+  static constexpr int kScaleCols = KIND == MX ? 4 + 4 * ((BN + 127) / 128) : 0;
+  static constexpr int kStages = (200 * 1024) / kStageBytes < 8 ? (200 * 1024) / kStageBytes : 8;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleStages * kScaleBytes + 512;
+  static_assert(2 * BN + kScaleStages * kScaleCols <= 512, "two sets of sums and the scales fit tensor memory");
+  static_assert(BN % 32 == 0 && kStageBytesC % 1024 == 0, "");
+};
+
+// Pairs of blocks (clusters of two, one block on each SM) take 256 x BN tiles in
+// turn.  Of each stage a block brings the 128 rows of R that its own tensor
+// memory sums up and half of the columns of C; one thread of the first block
+// issues the products for both (cta_group::2), so each byte of C is read from
+// shared memory by both SMs but copied there once: per SM 16 KB + 64 BN bytes
+// for 256 x BN x 128 bytes' worth of products, against 16 KB + 128 BN of a
+// block on its own, which would ask for more than the L2 delivers.  The sums
+// alternate between two halves of tensor memory, and warps 4 to 7 store one
+// tile while the next is computed.  Warps 2 and 3 bring the scales.
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ CUtensorMap map_r,
+                                                                const __grid_constant__ CUtensorMap map_c, const Params p) {
+  using S = PairShape<KIND, BN>;
+  constexpr bool SYM = EPI == GRAM || EPI == POLY;
+  constexpr int kElems = KIND == MX ? 128 : 64;
+  constexpr int kHalf = BN / 2;
+  static_assert(KIND == F16 || (!R_MN && !C_MN), "8-bit operands are K-major");
+  static_assert(!C_MN || kHalf % 64 == 0, "an MN-major box is 64 wide");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = tc::smem_addr(smem);
+  const uint32_t scales = ring + S::kStages * S::kStageBytes;
+  const uint32_t ctl = scales + S::kScaleStages * S::kScaleBytes;
+  const uint32_t full = ctl, empty = full + 8 * S::kStages, sfull = empty + 8 * S::kStages,
+                 sempty = sfull + 8 * S::kScaleStages, accfull = sempty + 8 * S::kScaleStages, accempty = accfull + 16,
+                 slot = accempty + 16;
+  volatile uint32_t* slot_p = reinterpret_cast<volatile uint32_t*>(smem + (slot - ring));
+  volatile int* fail = reinterpret_cast<volatile int*>(smem + (slot + 4 - ring));
+
+  tc::launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int all = p.tiles * p.batch;
+  const int blocks = (p.k + kElems - 1) / kElems;   // > 0
+
+  if (threadIdx.x == 0) {
+    tc::prefetch_map(&map_r);
+    tc::prefetch_map(&map_c);
+    for (int i = 0; i < S::kStages; ++i) {
+      tc::mbar_init(full + 8 * i, 1);
+      tc::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kScaleStages; ++i) {
+      tc::mbar_init(sfull + 8 * i, 4);      // two warps of each block
+      tc::mbar_init(sempty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(accfull + 8 * i, 1);
+      tc::mbar_init(accempty + 8 * i, 8);   // four warps of each block
+    }
+    *fail = 0;
+    tc::mbar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc<2, S::kTmemCols>(slot);
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after();
+  tc::wait_for_earlier();
+  const uint32_t acc = *slot_p;
+  const uint32_t tscale = acc + 2 * BN;
+  auto gave_up = [&]() {
+    *fail = 1;
+    atomicCAS(&g_dense_error, 0, kErrTimeout);
+  };
+  auto place = [&](int tile, int* r0, int* c0, int* batch, bool* mirror) {
+    const int b = tile / p.tiles, t = tile - b * p.tiles;
+    int tr, tcn;
+    *mirror = false;
+    if constexpr (SYM) {
+      symmetric_tile<2 * kRowsTile, BN>(t, &tr, &tcn, mirror);
+    } else {
+      tr = t % p.tiles_r;
+      tcn = t / p.tiles_r;
+    }
+    *r0 = tr * 2 * kRowsTile + (int)rank * kRowsTile;
+    *c0 = tcn * BN;
+    *batch = b;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < all && ok; tile += pairs) {
+        int r0, c0, batch;
+        bool mirror;
+        place(tile, &r0, &c0, &batch, &mirror);
+        const int ch = c0 + (int)rank * kHalf;
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const int s = it % S::kStages;
+          ok = tc::mbar_wait_cluster(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
+          if (!ok) break;
+          const uint32_t dst = ring + s * S::kStageBytes, bar = tc::map_rank(full + 8 * s, 0);
+          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * S::kStageBytes);   // both blocks' bytes
+          if (R_MN) {
+            tc::tma_load3_pair(dst, &map_r, r0, kb * kElems, batch, bar);
+            tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, kb * kElems, batch, bar);
+          } else {
+            tc::tma_load3_pair(dst, &map_r, kb * kElems, r0, batch, bar);
+          }
+          if (C_MN) {
+#pragma unroll
+            for (int i = 0; i < kHalf / 64; ++i)
+              tc::tma_load3_pair(dst + kStageBytesR + 8192 * i, &map_c, ch + 64 * i, kb * kElems, batch, bar);
+          } else {
+            tc::tma_load3_pair(dst + kStageBytesR, &map_c, kb * kElems, ch, batch, bar);
+          }
+        }
+      }
+      if (!ok) gave_up();
+      // no copy is in flight when the blocks leave: both blocks' complete on the first one's barriers,
+      // and the second does not leave before the first
+      if (rank == 0)
+        for (int i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+          tc::mbar_wait_cluster(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = KIND == MX ? tc::idesc_mx(256, BN, p.fmt_r, p.fmt_c) : tc::idesc_f16(256, BN, R_MN, C_MN);
+      int it = 0, groups = 0, n = 0;
+      uint32_t ts = 0;
+      bool ok = true;
+      for (int tile = pair; tile < all && ok; tile += pairs, ++n) {
+        const int half = n & 1;
+        ok = tc::mbar_wait_cluster(accempty + 8 * half, ((n >> 1) & 1) ^ 1);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = acc + half * BN;
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const int s = it % S::kStages;
+          ok = tc::mbar_wait_cluster(full + 8 * s, (it / S::kStages) & 1);
+          if (!ok) break;
+          if (KIND == MX && (kb & 3) == 0) {
+            const int ss = groups % S::kScaleStages;
+            ok = tc::mbar_wait_cluster(sfull + 8 * ss, (groups / S::kScaleStages) & 1);
+            if (!ok) break;
+            ++groups;
+            tc::fence_after();
+            ts = tscale + ss * S::kScaleCols;
+            const uint32_t src = scales + ss * S::kScaleBytes;
+            tc::copy_scales<2>(ts, tc::desc_scales(src));
+#pragma unroll
+            for (int i = 0; i < (BN + 127) / 128; ++i)
+              tc::copy_scales<2>(ts + 4 + 4 * i, tc::desc_scales(src + 512 + 512 * i));
+          }
+          tc::fence_after();
+          const uint32_t a = ring + s * S::kStageBytes;
+          stage_products<2, KIND, R_MN, C_MN>(d, a, a + kStageBytesR, KIND == MX ? tc::idesc_mx_id(idesc, kb & 3) : idesc,
+                                              ts, kb > 0);
+          tc::commit<2>(empty + 8 * s);
+          if (KIND == MX && ((kb & 3) == 3 || kb + 1 == blocks)) tc::commit<2>(sempty + 8 * ((groups - 1) % S::kScaleStages));
+        }
+        if (ok) tc::commit<2>(accfull + 8 * half);
+      }
+      if (!ok) {
+        gave_up();
+        tc::commit<2>(accfull);      // what was issued ends before the blocks leave (bounded by the readers' wait)
+        tc::mbar_wait_cluster(accfull, 0);
+      }
+    }
+  } else if (warp < 4) {
+    if (KIND == MX) {
+      const int t = threadIdx.x - 64;   // 0..63
+      const uint32_t peer_full = tc::map_rank(sfull, 0);
+      constexpr int kWords = 2 + 2 * ((BN + 127) / 128);
+      int n = 0;
+      bool ok = true;
+      for (int tile = pair; tile < all && ok; tile += pairs) {
+        int r0, c0, batch;
+        bool mirror;
+        place(tile, &r0, &c0, &batch, &mirror);
+        for (int g = 0; 4 * g < blocks; ++g, ++n) {
+          const int ss = n % S::kScaleStages;
+          uint32_t w[kWords];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            w[i] = scale_word(p.sr, p.ld_sr, p.shift_r, r0 + t + 64 * i, p.rows, g, blocks);
+#pragma unroll
+          for (int i = 2; i < kWords; ++i) {
+            const int c = t + 64 * (i - 2);
+            w[i] = scale_word(p.sc, p.ld_sc, p.shift_c, c < BN ? c0 + c : p.cols, p.cols, g, blocks);
+          }
+          ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(sempty + 8 * ss, ((n / S::kScaleStages) & 1) ^ 1));
+          if (!ok) break;
+          uint8_t* dst = smem + (scales - ring) + ss * S::kScaleBytes;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const int x = t + 64 * (i & 1);
+            *reinterpret_cast<uint32_t*>(dst + 512 * (i >> 1) + (x & 31) * 16 + (x >> 5) * 4) = w[i];
+          }
+          tc::fence_async_shared();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster(peer_full + 8 * ss);
+        }
+      }
+      if (!ok) gave_up();
+    }
+  } else {
+    const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
+    int n = 0;
+    bool ok = true;
+    for (int tile = pair; tile < all && ok; tile += pairs, ++n) {
+      int r0, c0, batch;
+      bool mirror;
+      place(tile, &r0, &c0, &batch, &mirror);
+      const int half = n & 1, row = r0 + 32 * (warp & 3) + lane;
+      Ahead ahead[2];
+      load_ahead<EPI>(p, batch, row, c0, ahead[0]);
+      ok = tc::mbar_wait_cluster(accfull + 8 * half, (n >> 1) & 1);
+      ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
+      if (!ok) break;
+      tc::fence_after();
+#pragma unroll
+      for (int g = 0; g < BN / 16; ++g) {
+        if (c0 + 16 * g >= p.cols) break;
+        if (g + 1 < BN / 16) load_ahead<EPI>(p, batch, row, c0 + 16 * g + 16, ahead[(g + 1) & 1]);
+        uint32_t u[16];
+        tc::tmem_ld16(sums + half * BN + 16 * g, u);
+        tc::tmem_wait_ld(u);
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g & 1], v);
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(accempty + 8 * half, 0));
+    }
+    if (!ok) gave_up();
+  }
+  __syncwarp();
+  __syncthreads();
+  tc::fence_before();
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::tmem_dealloc<2, S::kTmemCols>(acc);
   }
 }
 

@@ -53,8 +53,9 @@ struct QuantParams {
   int vec;                     // rows of x (and minus) start on 4-element boundaries
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kTile = 128;
+constexpr int kRows = 8;       // rows of a warp
 
 // Exponent of the block's scale from the largest |x| as fp32 bits: the least
 // e >= -127 with |x| <= FMAX 2^e, FMAX = 0.875 * 2^TOP (448 or 57344), 0 for a
@@ -84,7 +85,7 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return codes2<E5M2>(a, b) | (codes2<E5M2>(c, d) << 16);
 }
 
-// One block takes one 128 x 128 tile of x: warp w the rows 16 w .. 16 w + 15,
+// One block takes one 128 x 128 tile of x: warp w the rows 8 w .. 8 w + 7,
 // lane l the columns 4 l .. 4 l + 3, so a tile is read once, in 16-byte loads
 // that are all in flight at once, and stays in registers for both layouts.  The
 // largest |x| of a row is one warp reduction on the fp32 bits (for values that
@@ -94,23 +95,23 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // that neither side has bank conflicts.
 // ROW_BLOCKS: one scale for each row (or column) and 128 values; else one for the tile.
 template <int T, bool E5M2, bool ROW_BLOCKS>
-__global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 2) quantise_kernel(const QuantParams p) {
   constexpr int TOP = E5M2 ? 16 : 9;
-  __shared__ uint32_t most[8][kTile];
+  __shared__ uint32_t most[16][kTile];
   __shared__ uint32_t words[kTile][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
-  const int r0 = tr * kTile + warp * 16, c0 = tc * kTile, c = c0 + 4 * lane;
-  const int live = min(16, p.rows - r0);            // rows of this warp, may be <= 0
+  const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile, c = c0 + 4 * lane;
+  const int live = min(kRows, p.rows - r0);            // rows of this warp, may be <= 0
   using X = typename In<T>::type;
   const X* x = static_cast<const X*>(p.x) + (int64_t)r0 * p.ld_x + c;
-  float v[16][4];
-  if (live == 16 && c + 4 <= p.cols && p.vec) {
+  float v[kRows][4];
+  if (live == kRows && c + 4 <= p.cols && p.vec) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) In<T>::get4(x + (int64_t)i * p.ld_x, v[i]);
+    for (int i = 0; i < kRows; ++i) In<T>::get4(x + (int64_t)i * p.ld_x, v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         v[i][j] = (i < live && c + j < p.cols) ? In<T>::get(x[(int64_t)i * p.ld_x + j]) : 0.f;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
   if (p.minus != nullptr) {
     const float* m = p.minus + (int64_t)r0 * p.ld_minus + c;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       float u[4] = {0.f, 0.f, 0.f, 0.f};
       if (i < live) {
         if (c + 4 <= p.cols && p.vec) {
@@ -135,9 +136,9 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
   }
 
   uint32_t col[4] = {0, 0, 0, 0};
-  uint32_t rowb[16];                                 // row scales as bytes
+  uint32_t rowb[kRows];                                 // row scales as bytes
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kRows; ++i) {
     uint32_t b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -154,17 +155,17 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     __syncthreads();
     uint32_t a = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) a = max(a, most[w][0]);
+    for (int w = 0; w < 16; ++w) a = max(a, most[w][0]);
     tile_byte = scale_byte<TOP>(a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) rowb[i] = tile_byte;
+    for (int i = 0; i < kRows; ++i) rowb[i] = tile_byte;
   }
 
   if (p.q != nullptr) {
     if (ROW_BLOCKS) {
       if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kRows; ++i)
           if (i < live) p.s[(int64_t)(r0 + i) * p.ld_s + tc] = (uint8_t)rowb[i];
       }
     } else if (threadIdx.x == 0) {
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     }
     uint8_t* q = p.q + (int64_t)r0 * p.ld_q + c;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       if (i >= live) break;
       const float f = scale_factor(rowb[i]);
       const uint32_t w = codes4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
       for (int j = 0; j < 4; ++j) {
         uint32_t a = 0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a = max(a, most[w][4 * lane + j]);
+        for (int w = 0; w < 16; ++w) a = max(a, most[w][4 * lane + j]);
         colb[j] = scale_byte<TOP>(a);
         if (warp == 0 && c + j < p.cols) p.st[(int64_t)(c + j) * p.ld_st + tr] = (uint8_t)colb[j];
       }
@@ -208,14 +209,14 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
     for (int j = 0; j < 4; ++j) {
       const float f = scale_factor(colb[j]);
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        words[4 * lane + j][(warp * 4 + i / 4) ^ lane] = codes4<E5M2>(v[i][j] * f, v[i + 1][j] * f, v[i + 2][j] * f, v[i + 3][j] * f);
+      for (int i = 0; i < kRows; i += 4)
+        words[4 * lane + j][(warp * (kRows / 4) + i / 4) ^ lane] = codes4<E5M2>(v[i][j] * f, v[i + 1][j] * f, v[i + 2][j] * f, v[i + 3][j] * f);
     }
     __syncthreads();
     const int r = tr * kTile + 4 * lane;             // four rows of x, now columns
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int cl = warp * 16 + i;
+    for (int i = 0; i < kRows; ++i) {
+      const int cl = warp * kRows + i;
       if (c0 + cl >= p.cols) break;
       const uint32_t w = words[cl][lane ^ (cl >> 2)];
       uint8_t* q = p.qt + (int64_t)(c0 + cl) * p.ld_qt + r;
@@ -232,6 +233,9 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantParams p)
 
 // ------------------------------------------------------------ Muon's elementwise passes
 
+constexpr int kUpdateThreads = 256;
+constexpr int kSpan = 512;        // columns that a warp takes at a time
+
 struct UpdateParams {
   const void* g;
   float* momentum;         // or null: the update is g itself
@@ -239,36 +243,79 @@ struct UpdateParams {
   __half* x;               // [batch][rows][ld_x]
   int64_t ld_g, batch_g, ld_m, ld_x, batch_x;
   int rows, cols, parts;
+  int vec;                 // rows of g and momentum start on 4-element boundaries
   float mu;
   int nesterov;
   float eps, scale;
 };
 
-// u = g + mu momentum (nesterov) or momentum, from the momentum already updated; g without one.
+// u = g + mu momentum (nesterov) or momentum, from the momentum already updated.
 __device__ __forceinline__ float update_of(const UpdateParams& p, float g, float m) {
   return p.nesterov ? fmaf(p.mu, m, g) : m;
 }
 
+// Both passes read g (and the momentum) once: a warp takes 512 columns of a row at
+// a time, 16 values a lane in four 4-element loads that are in flight together.
+template <int T>
+__device__ __forceinline__ void load_span(const UpdateParams& p, const typename In<T>::type* g, const float* m, int c,
+                                          float (&u)[16], float (&mv)[16]) {
+  if (c + kSpan - 4 * (int)(threadIdx.x & 31) <= p.cols && p.vec) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) In<T>::get4(g + c + 128 * j, *reinterpret_cast<float(*)[4]>(&u[4 * j]));
+    if (m != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) In<IN_F32>::get4(m + c + 128 * j, *reinterpret_cast<float(*)[4]>(&mv[4 * j]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int at = c + 128 * (j / 4) + j % 4;
+      u[j] = at < p.cols ? In<T>::get(g[at]) : 0.f;
+      mv[j] = m != nullptr && at < p.cols ? m[at] : 0.f;
+    }
+  }
+}
+
 // First pass: updates the momentum (in place) and leaves each block's sum of squares of u.
 template <int T>
-__global__ void __launch_bounds__(256) norm_kernel(const UpdateParams p) {
+__global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams p) {
   using X = typename In<T>::type;
   __shared__ double part[8];
-  const int64_t n = (int64_t)p.rows * p.cols;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int spans = (p.cols + kSpan - 1) / kSpan;
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
   double sum = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / p.cols, c = i - r * p.cols;
-    float u = In<T>::get(g[r * p.ld_g + c]);
-    if (p.momentum != nullptr) {
-      const float m = fmaf(p.mu, p.momentum[r * p.ld_m + c], u);
-      p.momentum[r * p.ld_m + c] = m;
-      u = update_of(p, u, m);
+  for (int i = blockIdx.x * 8 + warp; i < p.rows * spans; i += gridDim.x * 8) {
+    const int r = i / spans, c = (i - r * spans) * kSpan + 4 * lane;
+    float u[16], m[16];
+    float* mp = p.momentum == nullptr ? nullptr : p.momentum + (int64_t)r * p.ld_m;
+    load_span<T>(p, g + (int64_t)r * p.ld_g, mp, c, u, m);
+    if (mp != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        m[j] = fmaf(p.mu, m[j], u[j]);
+        u[j] = update_of(p, u[j], m[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = c + 128 * j;
+        if (at + 4 <= p.cols && p.vec) {
+          *reinterpret_cast<float4*>(mp + at) = make_float4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (at + k < p.cols) mp[at + k] = m[4 * j + k];
+        }
+      }
     }
-    sum += (double)u * (double)u;
+    // squares in fp32, their sums in fp64 (16 at a time: nothing is lost to a long sum)
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s = fmaf(u[j], u[j], s);
+    sum += (double)s;
   }
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  if (lane == 0) part[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) sum += part[w];
@@ -278,25 +325,41 @@ __global__ void __launch_bounds__(256) norm_kernel(const UpdateParams p) {
 
 // Second pass: X_0 = u / (|u| + eps), scaled, as fp16.
 template <int T>
-__global__ void __launch_bounds__(256) start_kernel(const UpdateParams p) {
+__global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParams p) {
   using X = typename In<T>::type;
-  __shared__ float factor;
-  if (threadIdx.x < 32) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < p.parts; i += 32) s += p.partial[(int64_t)blockIdx.y * p.parts + i];
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (threadIdx.x == 0) factor = (float)((double)p.scale / (sqrt(s) + (double)p.eps));
-  }
+  __shared__ double part[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // every block adds up all parts in the same order
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < p.parts; i += kUpdateThreads) sum += p.partial[(int64_t)blockIdx.y * p.parts + i];
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) part[warp] = sum;
   __syncthreads();
-  const int64_t n = (int64_t)p.rows * p.cols;
+  sum = 0.0;
+  for (int w = 0; w < 8; ++w) sum += part[w];
+  const float f = (float)((double)p.scale / (sqrt(sum) + (double)p.eps));
+  const int spans = (p.cols + kSpan - 1) / kSpan;
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
   __half* x = p.x + blockIdx.y * p.batch_x;
-  const float f = factor;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / p.cols, c = i - r * p.cols;
-    float u = In<T>::get(g[r * p.ld_g + c]);
-    if (p.momentum != nullptr) u = update_of(p, u, p.momentum[r * p.ld_m + c]);
-    x[r * p.ld_x + c] = __float2half_rn(u * f);
+  for (int i = blockIdx.x * 8 + warp; i < p.rows * spans; i += gridDim.x * 8) {
+    const int r = i / spans, c = (i - r * spans) * kSpan + 4 * lane;
+    float u[16], m[16];
+    const float* mp = p.momentum == nullptr ? nullptr : p.momentum + (int64_t)r * p.ld_m;
+    load_span<T>(p, g + (int64_t)r * p.ld_g, mp, c, u, m);
+    __half* o = x + (int64_t)r * p.ld_x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = c + 128 * j;
+      if (at >= p.cols) break;
+      alignas(8) __half h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = mp == nullptr ? u[4 * j + k] : update_of(p, u[4 * j + k], m[4 * j + k]);
+        h[k] = __float2half_rn(v * f);
+      }
+      // rows of x have room for whole groups of 8
+      *reinterpret_cast<uint2*>(o + at) = *reinterpret_cast<const uint2*>(h);
+    }
   }
 }
 

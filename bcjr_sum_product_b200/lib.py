@@ -6,7 +6,6 @@ is no CPU fallback: if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -43,6 +42,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load the library (building it in-tree first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             from . import build as _build
@@ -253,11 +254,12 @@ def _matrix(t: torch.Tensor, name: str, dtypes, ndim: int = 2, device=None) -> t
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
-    if t.dim() != ndim:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    if t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+    if stride[-2] < shape[-1] and shape[-2] > 1:
         raise ValueError(f"the rows of {name} must not overlap")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -269,31 +271,33 @@ def _ld(t: torch.Tensor, multiple: int = 1) -> int:
     return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // multiple) * multiple
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """The call's device and stream: the tensors' device made current, the
-    given stream (or that device's current one) for allocations and launches."""
+def _call(device: torch.device, stream, fn, *args):
+    """fn(*args, stream handle) with the tensors' device current, on the given
+    stream or that device's current one (allocations belong to it too)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
-                raise ValueError(f"stream must be on {device}")
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+            return fn(*args, torch.cuda.current_stream().cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, stream.cuda_stream)
 
 
-def _code_room(rows: int, cols: int, dtype, device) -> torch.Tensor:
-    """[rows, cols] codes in rows of a multiple of 16 bytes."""
-    return torch.empty((rows, -(-cols // 16) * 16), dtype=dtype, device=device)[:, :cols]
+def _codes_room(rows: int, cols: int, block_rows: int, dtype, device):
+    """Codes [rows, cols] in rows of a multiple of 16 bytes, scales in rows of a
+    multiple of 4; and pointer and row stride of each for the call."""
+    ld, blocks = -(-cols // 16) * 16, -(-cols // _BLOCK)
+    ld_s = -(-blocks // 4) * 4
+    q = torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device)
+    s = torch.empty_strided((-(-rows // block_rows), blocks), (ld_s, 1), dtype=torch.float8_e8m0fnu, device=device)
+    return (q, s), (q.data_ptr(), ld, s.data_ptr(), ld_s)
 
 
-def _scale_room(rows: int, cols: int, block_rows: int, device) -> torch.Tensor:
-    """One scale for each block, in rows of a multiple of 4 bytes."""
-    n = -(-cols // _BLOCK)
-    return torch.empty((-(-rows // block_rows), -(-n // 4) * 4), dtype=torch.float8_e8m0fnu, device=device)[:, :n]
+_NO_CODES = ((), (None, 0, None, 0))
 
 
 def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float8_e4m3fn,
@@ -318,19 +322,18 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
         _matrix(minus, "minus", (torch.float32,), device=x.device)
         if minus.shape != x.shape:
             raise ValueError("minus must have the shape of x")
+    return _call(x.device, stream, _fp8_quantise, x, block_rows, dtype, minus, layout)
+
+
+def _fp8_quantise(x, block_rows, dtype, minus, layout, st):
     rows, cols = x.shape
-    with _on(x.device, stream) as st:
-        q = s = qt = s_t = None
-        if layout != "cols":
-            q, s = _code_room(rows, cols, dtype, x.device), _scale_room(rows, cols, block_rows, x.device)
-        if layout != "rows":
-            qt, s_t = _code_room(cols, rows, dtype, x.device), _scale_room(cols, rows, block_rows, x.device)
-        rc = load().bcjr_fp8_quantise(
-            _ptr(x), _TYPES[x.dtype], rows, cols, _ld(x), _ptr(minus), 0 if minus is None else _ld(minus),
-            _TYPES[dtype], block_rows, _ptr(q), 0 if q is None else q.stride(0), _ptr(s), 0 if s is None else s.stride(0),
-            _ptr(qt), 0 if qt is None else qt.stride(0), _ptr(s_t), 0 if s_t is None else s_t.stride(0), st)
+    out, room = _codes_room(rows, cols, block_rows, dtype, x.device) if layout != "cols" else _NO_CODES
+    out_t, room_t = _codes_room(cols, rows, block_rows, dtype, x.device) if layout != "rows" else _NO_CODES
+    rc = load().bcjr_fp8_quantise(
+        x.data_ptr(), _TYPES[x.dtype], rows, cols, _ld(x), None if minus is None else minus.data_ptr(),
+        0 if minus is None else _ld(minus), _TYPES[dtype], block_rows, *room, *room_t, st)
     _check(rc, "bcjr_fp8_quantise")
-    return (q, s) if layout == "rows" else (qt, s_t) if layout == "cols" else (q, s, qt, s_t)
+    return out + out_t
 
 
 def _scaled(q: torch.Tensor, scale: torch.Tensor, name: str, device) -> int:
@@ -365,13 +368,17 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
         _matrix(out, "out", _WIDE, device=a.device)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
-    with _on(a.device, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-        rc = load().bcjr_fp8_matmul(
-            _ptr(a), _TYPES[a.dtype], _ld(a, 16), _ptr(scale_a), _ld(scale_a), a_rows, _ptr(b), _TYPES[b.dtype],
-            _ld(b, 16), _ptr(scale_b), _ld(scale_b), b_rows, M, N, K, float(alpha), _ptr(out), _TYPES[out.dtype],
-            _ld(out), st)
+    return _call(a.device, stream, _fp8_matmul, a, scale_a, a_rows, b, scale_b, b_rows, alpha, out_dtype, out)
+
+
+def _fp8_matmul(a, scale_a, a_rows, b, scale_b, b_rows, alpha, out_dtype, out, st):
+    (M, K), N = a.shape, b.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    rc = load().bcjr_fp8_matmul(
+        a.data_ptr(), _TYPES[a.dtype], _ld(a, 16), scale_a.data_ptr(), _ld(scale_a), a_rows, b.data_ptr(),
+        _TYPES[b.dtype], _ld(b, 16), scale_b.data_ptr(), _ld(scale_b), b_rows, M, N, K, alpha, out.data_ptr(),
+        _TYPES[out.dtype], _ld(out), st)
     _check(rc, "bcjr_fp8_matmul")
     return out
 
@@ -400,14 +407,15 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = 
     _matrix(g, "g", _WIDE, ndim=g.dim())
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float16")
+    return _call(g.device, stream, _orthogonalise, g, int(steps), _coeffs(coeffs, steps), eps, out_dtype)
+
+
+def _orthogonalise(g, steps, coeffs, eps, out_dtype, st):
     rows, cols = g.shape[-2:]
-    batch = g.shape[0] if g.dim() == 3 else 1
-    co = _coeffs(coeffs, steps)
-    with _on(g.device, stream) as st:
-        out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
-        rc = load().bcjr_orthogonalise(_ptr(g), _TYPES[g.dtype], batch, rows, cols, _ld(g),
-                                       g.stride(0) if g.dim() == 3 else 0, int(steps), co, float(eps), _ptr(out),
-                                       _TYPES[out_dtype], cols, rows * cols, st)
+    out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
+    batch, stride = (g.shape[0], g.stride(0)) if g.dim() == 3 else (1, 0)
+    rc = load().bcjr_orthogonalise(g.data_ptr(), _TYPES[g.dtype], batch, rows, cols, _ld(g), stride, steps, coeffs, eps,
+                                   out.data_ptr(), _TYPES[out_dtype], cols, rows * cols, st)
     _check(rc, "bcjr_orthogonalise")
     return out
 
@@ -428,10 +436,13 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: f
     rows, cols = w.shape
     if scale is None:
         scale = math.sqrt(max(1.0, rows / cols)) if cols else 1.0
-    co = _coeffs(coeffs, steps)
-    with _on(w.device, stream) as st:
-        rc = load().bcjr_muon_step(_ptr(w), _ld(w), _ptr(grad), _TYPES[grad.dtype], _ld(grad), _ptr(momentum),
-                                   _ld(momentum), rows, cols, float(lr), float(mu), int(bool(nesterov)),
-                                   float(weight_decay), float(scale), int(steps), co, float(eps), st)
+    return _call(w.device, stream, _muon_step, w, grad, momentum, lr, mu, int(bool(nesterov)), weight_decay, scale,
+                 int(steps), _coeffs(coeffs, steps), eps)
+
+
+def _muon_step(w, grad, momentum, lr, mu, nesterov, weight_decay, scale, steps, coeffs, eps, st):
+    rows, cols = w.shape
+    rc = load().bcjr_muon_step(w.data_ptr(), _ld(w), grad.data_ptr(), _TYPES[grad.dtype], _ld(grad), momentum.data_ptr(),
+                               _ld(momentum), rows, cols, lr, mu, nesterov, weight_decay, scale, steps, coeffs, eps, st)
     _check(rc, "bcjr_muon_step")
     return w, momentum
