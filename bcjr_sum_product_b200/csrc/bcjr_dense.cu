@@ -182,7 +182,12 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
-  return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, chained, mr, mc, p, st);
+  // The pairs that run together work on neighbouring columns of all of R, which then has to stay in
+  // L2 (126 MB); a larger R is taken in bands of 16 tiles (8-bit 8192 x 8192 x 8192: 492 -> 446 us;
+  // with k = 2048, where R is 16 MB, bands cost 3 %).
+  G::Params pb = p;
+  pb.band = r.inner * r.outer * elem > ((int64_t)48 << 20) ? std::min(p.tiles_r, 16) : p.tiles_r;
+  return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, chained, mr, mc, pb, st);
 }
 
 // Blocks of one tile: as many (1, 2, 4 or 8) as the tiles leave room for, each with at least two stages of k.
@@ -270,6 +275,7 @@ int sym_tile(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
 template <int BN, int EPI, bool MN>
 int sym_pair(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, 2 * G::kRowsTile);
+  p.tiles_r = (int)t;
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
   return launch_pair<G::F16, BN, MN, MN, EPI>(x, x, p, nsm, true, st);
 }

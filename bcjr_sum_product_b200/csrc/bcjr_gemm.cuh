@@ -59,6 +59,7 @@ struct Params {
   int tiles;                 // tiles of one matrix
   int batch;
   int splits;                // blocks of one tile (the cluster of tile_kernel)
+  int band;                  // pair_kernel: tiles along r of a band
   // MX
   const uint8_t* sr;         // scales of R: sr[(r >> shift_r) * ld_sr + k / 128]
   const uint8_t* sc;
@@ -200,11 +201,11 @@ __device__ __forceinline__ void symmetric_tile(int t, int* tr, int* tc, bool* mi
 // The products of one stage: four instructions of 32 bytes of k.
 template <int CG, int KIND, bool R_MN, bool C_MN>
 __device__ __forceinline__ void stage_products(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, uint32_t ts, bool add) {
+  const uint64_t da0 = tc::desc_sw128(a, R_MN ? 8192 : 0), db0 = tc::desc_sw128(b, C_MN ? 8192 : 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // 32 bytes along K, or 16 rows of 128 bytes where K runs over the rows
-    const uint64_t da = tc::desc_sw128(a + i * (R_MN ? 2048 : 32), R_MN ? 8192 : 0);
-    const uint64_t db = tc::desc_sw128(b + i * (C_MN ? 2048 : 32), C_MN ? 8192 : 0);
+    const uint64_t da = da0 + i * (R_MN ? 128 : 2), db = db0 + i * (C_MN ? 128 : 2);
     if (KIND == MX) tc::mma_mx<CG>(acc, da, db, idesc, ts, ts + 4, add || i > 0);
     else tc::mma_f16<CG>(acc, da, db, idesc, add || i > 0);
   }
@@ -331,36 +332,41 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         tc::mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = KIND == MX ? tc::idesc_mx(128, BN, p.fmt_r, p.fmt_c) : tc::idesc_f16(128, BN, R_MN, C_MN);
-      int it = 0, group = -1, groups = 0;
-      uint32_t ts = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % S::kStages;
-        ok = tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1);
+    const uint32_t idesc = KIND == MX ? tc::idesc_mx(128, BN, p.fmt_r, p.fmt_c) : tc::idesc_f16(128, BN, R_MN, C_MN);
+    int it = 0, group = -1, groups = 0;
+    uint32_t ts = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int s = it % S::kStages;
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1));
+      if (!ok) break;
+      if (KIND == MX && group != kb / 4) {
+        group = kb / 4;
+        const int ss = groups % S::kScaleStages;
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(sfull + 8 * ss, (groups / S::kScaleStages) & 1));
         if (!ok) break;
-        if (KIND == MX && group != kb / 4) {
-          group = kb / 4;
-          const int ss = groups % S::kScaleStages;
-          ok = tc::mbar_wait(sfull + 8 * ss, (groups / S::kScaleStages) & 1);
-          if (!ok) break;
-          ++groups;
-          tc::fence_after();
-          ts = tscale + ss * S::kScaleCols;
+        ++groups;
+        tc::fence_after();
+        ts = tscale + ss * S::kScaleCols;
+        if (tc::elect_one()) {
           tc::copy_scales<1>(ts, tc::desc_scales(scales + ss * S::kScaleBytes));
           tc::copy_scales<1>(ts + 4, tc::desc_scales(scales + ss * S::kScaleBytes + 512));
         }
-        tc::fence_after();
+        __syncwarp();
+      }
+      tc::fence_after();
+      if (tc::elect_one()) {
         const uint32_t a = ring + s * S::kStageBytes;
         stage_products<1, KIND, R_MN, C_MN>(acc, a, a + kStageBytesR, KIND == MX ? tc::idesc_mx_id(idesc, kb & 3) : idesc,
                                             ts, it > 0);
         tc::commit<1>(empty + 8 * s);
         if (KIND == MX && ((kb & 3) == 3 || kb + 1 == kb1)) tc::commit<1>(sempty + 8 * ((groups - 1) % S::kScaleStages));
       }
-      if (!ok) gave_up();
-      tc::commit<1>(done);
+      __syncwarp();
     }
+    if (!ok) gave_up();
+    if (tc::elect_one()) tc::commit<1>(done);
+    __syncwarp();
   } else {
     const int t = threadIdx.x - 64;   // 0..127
     bool ok = true;
@@ -463,20 +469,22 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
 
 // ------------------------------------------------------------ large products
 
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 384;
 
 template <int KIND, int BN>
 struct PairShape {
-  static constexpr int kStageBytesC = BN / 2 * 128;             // a block brings half of the columns
-  static constexpr int kStageBytes = kStageBytesR + kStageBytesC;
+  static constexpr int kSub = 2;                                // 128-byte blocks of k in a stage
+  static constexpr int kSubBytes = kStageBytesR + BN / 2 * 128;  // a block of the pair brings half of the columns
+  static constexpr int kStageBytes = kSub * kSubBytes;
+  static constexpr int kStages = (200 * 1024) / kStageBytes;
   static constexpr int kScaleStages = 2;
   static constexpr int kScaleBytes = KIND == MX ? 512 + 512 * ((BN + 127) / 128) : 0;
   static constexpr int kScaleCols = KIND == MX ? 4 + 4 * ((BN + 127) / 128) : 0;
-  static constexpr int kStages = (200 * 1024) / kStageBytes < 8 ? (200 * 1024) / kStageBytes : 8;
+  static constexpr int kSets = 2 * BN + kScaleStages * kScaleCols <= 512 ? 2 : 1;   // sets of sums
   static constexpr int kTmemCols = 512;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleStages * kScaleBytes + 512;
-  static_assert(2 * BN + kScaleStages * kScaleCols <= 512, "two sets of sums and the scales fit tensor memory");
-  static_assert(BN % 32 == 0 && kStageBytesC % 1024 == 0, "");
+  static_assert(kStages >= 3, "the scales' waits need three stages");
+  static_assert(BN % 32 == 0 && kSubBytes % 1024 == 0, "");
 };
 
 // Pairs of blocks (clusters of two, one block on each SM) take 256 x BN tiles in
@@ -486,8 +494,10 @@ struct PairShape {
 // shared memory by both SMs but copied there once: per SM 16 KB + 64 BN bytes
 // for 256 x BN x 128 bytes' worth of products, against 16 KB + 128 BN of a
 // block on its own, which would ask for more than the L2 delivers.  The sums
-// alternate between two halves of tensor memory, and warps 4 to 7 store one
-// tile while the next is computed.  Warps 2 and 3 bring the scales.
+// alternate between two halves of tensor memory, and warps 4 to 11 store one
+// tile while the next is computed.  Warps 2 and 3 bring the scales.  A stage holds
+// two blocks of k, since every commit (the hand-back of a stage) makes the tensor
+// cores pause: about 0.13 us each, measured.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ CUtensorMap map_r,
                                                                 const __grid_constant__ CUtensorMap map_c, const Params p) {
@@ -503,8 +513,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   const uint32_t scales = ring + S::kStages * S::kStageBytes;
   const uint32_t ctl = scales + S::kScaleStages * S::kScaleBytes;
   const uint32_t full = ctl, empty = full + 8 * S::kStages, sfull = empty + 8 * S::kStages,
-                 sempty = sfull + 8 * S::kScaleStages, accfull = sempty + 8 * S::kScaleStages, accempty = accfull + 16,
-                 slot = accempty + 16;
+                 accfull = sfull + 8 * S::kScaleStages, accempty = accfull + 16, slot = accempty + 16;
   volatile uint32_t* slot_p = reinterpret_cast<volatile uint32_t*>(smem + (slot - ring));
   volatile int* fail = reinterpret_cast<volatile int*>(smem + (slot + 4 - ring));
 
@@ -522,13 +531,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       tc::mbar_init(full + 8 * i, 1);
       tc::mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < S::kScaleStages; ++i) {
-      tc::mbar_init(sfull + 8 * i, 4);      // two warps of each block
-      tc::mbar_init(sempty + 8 * i, 1);
-    }
+    for (int i = 0; i < S::kScaleStages; ++i) tc::mbar_init(sfull + 8 * i, 4);   // two warps of each block
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(accfull + 8 * i, 1);
-      tc::mbar_init(accempty + 8 * i, 8);   // four warps of each block
+      tc::mbar_init(accempty + 8 * i, 16);  // eight warps of each block
     }
     *fail = 0;
     tc::mbar_init_fence();
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   tc::fence_after();
   tc::wait_for_earlier();
   const uint32_t acc = *slot_p;
-  const uint32_t tscale = acc + 2 * BN;
+  const uint32_t tscale = acc + S::kSets * BN;
   auto gave_up = [&]() {
     *fail = 1;
     atomicCAS(&g_dense_error, 0, kErrTimeout);
@@ -552,8 +558,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     if constexpr (SYM) {
       symmetric_tile<2 * kRowsTile, BN>(t, &tr, &tcn, mirror);
     } else {
-      tr = t % p.tiles_r;
-      tcn = t / p.tiles_r;
+      // bands of `band` tiles along r, column by column: the pairs that run together share rows and columns
+      const int tiles_c = p.tiles / p.tiles_r, band = t / (p.band * tiles_c), in = t - band * p.band * tiles_c;
+      const int high = min(p.band, p.tiles_r - band * p.band);
+      tcn = in / high;
+      tr = band * p.band + in - tcn * high;
     }
     *r0 = tr * 2 * kRowsTile + (int)rank * kRowsTile;
     *c0 = tcn * BN;
@@ -569,24 +578,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         bool mirror;
         place(tile, &r0, &c0, &batch, &mirror);
         const int ch = c0 + (int)rank * kHalf;
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const int s = it % S::kStages;
-          ok = tc::mbar_wait_cluster(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
+        for (int kb = 0; kb < blocks; kb += S::kSub, ++it) {
+          const int s = it % S::kStages, n = min(S::kSub, blocks - kb);
+          ok = tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
           if (!ok) break;
-          const uint32_t dst = ring + s * S::kStageBytes, bar = tc::map_rank(full + 8 * s, 0);
-          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * S::kStageBytes);   // both blocks' bytes
-          if (R_MN) {
-            tc::tma_load3_pair(dst, &map_r, r0, kb * kElems, batch, bar);
-            tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, kb * kElems, batch, bar);
-          } else {
-            tc::tma_load3_pair(dst, &map_r, kb * kElems, r0, batch, bar);
-          }
-          if (C_MN) {
+          const uint32_t bar = tc::map_rank(full + 8 * s, 0);
+          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * n * S::kSubBytes);   // both blocks' bytes
+          for (int j = 0; j < n; ++j) {
+            const uint32_t dst = ring + s * S::kStageBytes + j * S::kSubBytes;
+            const int k = (kb + j) * kElems;
+            if (R_MN) {
+              tc::tma_load3_pair(dst, &map_r, r0, k, batch, bar);
+              tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, k, batch, bar);
+            } else {
+              tc::tma_load3_pair(dst, &map_r, k, r0, batch, bar);
+            }
+            if (C_MN) {
 #pragma unroll
-            for (int i = 0; i < kHalf / 64; ++i)
-              tc::tma_load3_pair(dst + kStageBytesR + 8192 * i, &map_c, ch + 64 * i, kb * kElems, batch, bar);
-          } else {
-            tc::tma_load3_pair(dst + kStageBytesR, &map_c, kb * kElems, ch, batch, bar);
+              for (int i = 0; i < kHalf / 64; ++i)
+                tc::tma_load3_pair(dst + kStageBytesR + 8192 * i, &map_c, ch + 64 * i, k, batch, bar);
+            } else {
+              tc::tma_load3_pair(dst + kStageBytesR, &map_c, k, ch, batch, bar);
+            }
           }
         }
       }
@@ -595,50 +608,62 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       // and the second does not leave before the first
       if (rank == 0)
         for (int i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-          tc::mbar_wait_cluster(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
+          tc::mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = KIND == MX ? tc::idesc_mx(256, BN, p.fmt_r, p.fmt_c) : tc::idesc_f16(256, BN, R_MN, C_MN);
       int it = 0, groups = 0, n = 0;
       uint32_t ts = 0;
       bool ok = true;
       for (int tile = pair; tile < all && ok; tile += pairs, ++n) {
-        const int half = n & 1;
-        ok = tc::mbar_wait_cluster(accempty + 8 * half, ((n >> 1) & 1) ^ 1);
+        const int set = n % S::kSets;
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(accempty + 8 * set, ((n / S::kSets) & 1) ^ 1));
         if (!ok) break;
         tc::fence_after();
-        const uint32_t d = acc + half * BN;
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
+        const uint32_t d = acc + set * BN;
+        for (int kb = 0; kb < blocks; kb += S::kSub, ++it) {
           const int s = it % S::kStages;
-          ok = tc::mbar_wait_cluster(full + 8 * s, (it / S::kStages) & 1);
+          ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1));
           if (!ok) break;
           if (KIND == MX && (kb & 3) == 0) {
             const int ss = groups % S::kScaleStages;
-            ok = tc::mbar_wait_cluster(sfull + 8 * ss, (groups / S::kScaleStages) & 1);
+            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(sfull + 8 * ss, (groups / S::kScaleStages) & 1));
             if (!ok) break;
             ++groups;
-            tc::fence_after();
             ts = tscale + ss * S::kScaleCols;
             const uint32_t src = scales + ss * S::kScaleBytes;
-            tc::copy_scales<2>(ts, tc::desc_scales(src));
+            tc::fence_after();
+            if (tc::elect_one()) {
+              tc::copy_scales<2>(ts, tc::desc_scales(src));
 #pragma unroll
-            for (int i = 0; i < (BN + 127) / 128; ++i)
-              tc::copy_scales<2>(ts + 4 + 4 * i, tc::desc_scales(src + 512 + 512 * i));
+              for (int i = 0; i < (BN + 127) / 128; ++i)
+                tc::copy_scales<2>(ts + 4 + 4 * i, tc::desc_scales(src + 512 + 512 * i));
+            }
+            __syncwarp();
+          } else {
+            tc::fence_after();
           }
-          tc::fence_after();
-          const uint32_t a = ring + s * S::kStageBytes;
-          stage_products<2, KIND, R_MN, C_MN>(d, a, a + kStageBytesR, KIND == MX ? tc::idesc_mx_id(idesc, kb & 3) : idesc,
-                                              ts, kb > 0);
-          tc::commit<2>(empty + 8 * s);
-          if (KIND == MX && ((kb & 3) == 3 || kb + 1 == blocks)) tc::commit<2>(sempty + 8 * ((groups - 1) % S::kScaleStages));
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int j = 0; j < S::kSub; ++j) {
+              if (kb + j < blocks) {
+                const uint32_t a = ring + s * S::kStageBytes + j * S::kSubBytes;
+                stage_products<2, KIND, R_MN, C_MN>(d, a, a + kStageBytesR,
+                                                    KIND == MX ? tc::idesc_mx_id(idesc, (kb + j) & 3) : idesc, ts, kb + j > 0);
+              }
+            }
+            tc::commit<2>(empty + 8 * s);
+          }
+          __syncwarp();
         }
-        if (ok) tc::commit<2>(accfull + 8 * half);
+        if (ok && tc::elect_one()) tc::commit<2>(accfull + 8 * set);
+        __syncwarp();
       }
       if (!ok) {
         gave_up();
-        tc::commit<2>(accfull);      // what was issued ends before the blocks leave (bounded by the readers' wait)
-        tc::mbar_wait_cluster(accfull, 0);
+        if (tc::elect_one()) tc::commit<2>(accfull);      // what was issued ends before the blocks leave (bounded by the readers' wait)
+        tc::mbar_wait(accfull, 0);
       }
     }
   } else if (warp < 4) {
@@ -646,7 +671,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       const int t = threadIdx.x - 64;   // 0..63
       const uint32_t peer_full = tc::map_rank(sfull, 0);
       constexpr int kWords = 2 + 2 * ((BN + 127) / 128);
-      int n = 0;
+      int n = 0, stage = 0;              // groups and stages so far
+      int last1 = -1, last2 = -1;        // last stages of the last two groups
       bool ok = true;
       for (int tile = pair; tile < all && ok; tile += pairs) {
         int r0, c0, batch;
@@ -663,8 +689,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
             const int c = t + 64 * (i - 2);
             w[i] = scale_word(p.sc, p.ld_sc, p.shift_c, c < BN ? c0 + c : p.cols, p.cols, g, blocks);
           }
-          ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(sempty + 8 * ss, ((n / S::kScaleStages) & 1) ^ 1));
+          // The slot is free once the stages of the group before last have been used up, which their own
+          // barriers tell (a commit for the slot alone would cost the tensor cores another pause).  Stage
+          // last2 + kStages belongs to this group or a later one, so that barrier is at most one phase ahead.
+          ok = last2 < 0 || tc::mbar_wait(empty + 8 * (last2 % S::kStages), (last2 / S::kStages) & 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
+          last2 = last1;
+          stage += min(2, (blocks - 4 * g + S::kSub - 1) / S::kSub);
+          last1 = stage - 1;
           uint8_t* dst = smem + (scales - ring) + ss * S::kScaleBytes;
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
@@ -679,35 +712,43 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       if (!ok) gave_up();
     }
   } else {
+    // eight warps: two for each quarter of the lanes, in turn on groups of 16 columns; the next
+    // group's sums (and what else its end reads) are loaded while this one is stored
     const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int first = (warp - 4) >> 2;
     int n = 0;
     bool ok = true;
     for (int tile = pair; tile < all && ok; tile += pairs, ++n) {
       int r0, c0, batch;
       bool mirror;
       place(tile, &r0, &c0, &batch, &mirror);
-      const int half = n & 1, row = r0 + 32 * (warp & 3) + lane;
+      const int set = n % S::kSets, row = r0 + 32 * (warp & 3) + lane;
       Ahead ahead[2];
-      load_ahead<EPI>(p, batch, row, c0, ahead[0]);
-      ok = tc::mbar_wait_cluster(accfull + 8 * half, (n >> 1) & 1);
+      uint32_t u[2][16];
+      load_ahead<EPI>(p, batch, row, c0 + 16 * first, ahead[0]);
+      ok = tc::mbar_wait(accfull + 8 * set, (n / S::kSets) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
       if (!ok) break;
       tc::fence_after();
+      tc::tmem_ld16(sums + set * BN + 16 * first, u[0]);
 #pragma unroll
-      for (int g = 0; g < BN / 16; ++g) {
-        if (c0 + 16 * g >= p.cols) break;
-        if (g + 1 < BN / 16) load_ahead<EPI>(p, batch, row, c0 + 16 * g + 16, ahead[(g + 1) & 1]);
-        uint32_t u[16];
-        tc::tmem_ld16(sums + half * BN + 16 * g, u);
-        tc::tmem_wait_ld(u);
+      for (int i = 0; i < BN / 32; ++i) {
+        const int c = 32 * i + 16 * first;
+        if (c0 + c >= p.cols) break;
+        tc::tmem_wait_ld(u[i & 1]);
+        if (i + 1 < BN / 32) {
+          tc::tmem_ld16(sums + set * BN + c + 32, u[(i + 1) & 1]);
+          load_ahead<EPI>(p, batch, row, c0 + c + 32, ahead[(i + 1) & 1]);
+        }
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g & 1], v);
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[i & 1][k]);
+        finish16<EPI>(p, batch, row, c0 + c, mirror, ahead[i & 1], v);
       }
+      tc::tmem_drain_ld();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(accempty + 8 * half, 0));
+      if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(accempty + 8 * set, 0));
     }
     if (!ok) gave_up();
   }
