@@ -85,84 +85,79 @@ __device__ __forceinline__ void store_one(void* out, int64_t i, float v) {
   else if (T == OUT_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
 }
-template <int T>
-__device__ __forceinline__ void store16(void* out, int64_t at, int64_t ld, int n, const float (&v)[16]) {
-  if (n >= 16) {
+template <int T, int W>
+__device__ __forceinline__ void store_columns(void* out, int64_t at, int64_t ld, int n, const float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) store_one<T>(out, at + (int64_t)i * ld, v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) store_one<T>(out, at + (int64_t)i * ld, v[i]);
+  for (int i = 0; i < W; ++i) {
+    if (i < n) store_one<T>(out, at, v[i]);
+    at += ld;
   }
 }
-__device__ __forceinline__ void store16_as(int type, void* out, int64_t at, int64_t ld, int n, const float (&v)[16]) {
-  if (type == OUT_F32) store16<OUT_F32>(out, at, ld, n, v);
-  else if (type == OUT_F16) store16<OUT_F16>(out, at, ld, n, v);
-  else store16<OUT_BF16>(out, at, ld, n, v);
-}
 
-// What the epilogue of columns c0..c0+15 of row r reads, loaded ahead: 16 entries
-// of row r of P (symmetric, so they lie side by side; ld_x is a multiple of 8).
+// What the end of W columns of a row reads, loaded ahead: W entries of row r of P
+// (symmetric, so they lie side by side; ld_x is a multiple of 8).
+template <int W>
 struct Ahead {
-  uint4 h[2];
+  uint4 h[W / 8];
 };
-template <int EPI>
-__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead& a) {
+template <int EPI, int W>
+__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W>& a) {
   if (EPI == POLY && r < p.rows) {
     const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x + c0;
-    a.h[0] = c0 < p.cols ? *reinterpret_cast<const uint4*>(x) : make_uint4(0, 0, 0, 0);
-    a.h[1] = c0 + 8 < p.cols ? *reinterpret_cast<const uint4*>(x + 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i)
+      a.h[i] = c0 + 8 * i < p.cols ? *reinterpret_cast<const uint4*>(x + 8 * i) : make_uint4(0, 0, 0, 0);
   }
 }
 
-// Stores columns c0..c0+15 (as far as they exist) of row r.
-template <int EPI>
-__device__ __forceinline__ void finish16(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead& a,
-                                         float (&v)[16]) {
+// Stores columns c0..c0+W-1 (as far as they exist) of row r.
+template <int EPI, int W>
+__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead<W>& a,
+                                       float (&v)[W]) {
   if (r >= p.rows) return;
   const int n = p.cols - c0;
   const int64_t at = batch * p.batch_out + (int64_t)c0 * p.ld_out + r;
   const float unit = EPI == OUT ? p.fa : EPI == LAST ? 1.f / (kIterScale * kIterScale) : 1.f / kIterScale;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] *= unit;
+  for (int i = 0; i < W; ++i) v[i] *= unit;
   if constexpr (EPI == OUT || EPI == LAST) {
-    store16_as(p.out_type, p.out, at, p.ld_out, n, v);
+    if (p.out_type == OUT_F32) store_columns<OUT_F32, W>(p.out, at, p.ld_out, n, v);
+    else if (p.out_type == OUT_F16) store_columns<OUT_F16, W>(p.out, at, p.ld_out, n, v);
+    else store_columns<OUT_BF16, W>(p.out, at, p.ld_out, n, v);
   } else if constexpr (EPI == GRAM || EPI == POLY || EPI == ITER) {
     if constexpr (EPI == POLY) {
       const __half* x = reinterpret_cast<const __half*>(a.h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < W; ++i) {
         v[i] = fmaf(p.fb, __half2float(x[i]), p.fc * v[i]);
         if (c0 + i == r) v[i] += p.fa * kIterScale;
       }
     }
-    alignas(16) __half h[16];
+    alignas(16) __half h[W];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = __float2half_rn(v[i]);
+    for (int i = 0; i < W; ++i) h[i] = __float2half_rn(v[i]);
     __half* o = static_cast<__half*>(p.out) + at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) o[(int64_t)i * p.ld_out] = h[i];
+    for (int i = 0; i < W; ++i) {
+      if (i < n) *o = h[i];
+      o += p.ld_out;
+    }
     if (EPI != ITER && mirror) {
       __half* m = static_cast<__half*>(p.out) + batch * p.batch_out + (int64_t)r * p.ld_out + c0;   // 16-byte aligned
-      if (n >= 16) {
-        reinterpret_cast<uint4*>(m)[0] = reinterpret_cast<const uint4*>(h)[0];
-        reinterpret_cast<uint4*>(m)[1] = reinterpret_cast<const uint4*>(h)[1];
-      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) m[i] = h[i];
+      for (int j = 0; j < W / 8; ++j) {
+        // whole groups of 8 stay inside the row's room (ld_out is the columns rounded up to 8)
+        if (8 * j < n) reinterpret_cast<uint4*>(m)[j] = reinterpret_cast<const uint4*>(h)[j];
       }
     }
   } else {   // STEP
     float* w = static_cast<float*>(p.out) + at;
-    float wv[16];
+    float wv[W];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) wv[i] = i < n ? w[(int64_t)i * p.ld_out] : 0.f;
+    for (int i = 0; i < W; ++i) wv[i] = i < n ? w[(int64_t)i * p.ld_out] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = fmaf(-p.rate * (1.f / kIterScale), v[i], p.keep * wv[i]);
-    store16<OUT_F32>(p.out, at, p.ld_out, n, v);
+    for (int i = 0; i < W; ++i) v[i] = fmaf(-p.rate * (1.f / kIterScale), v[i], p.keep * wv[i]);
+    store_columns<OUT_F32, W>(p.out, at, p.ld_out, n, v);
   }
 }
 
@@ -213,7 +208,7 @@ __device__ __forceinline__ void stage_products(uint32_t acc, uint32_t a, uint32_
 
 // ------------------------------------------------------------ small products
 
-constexpr int kTileThreads = 192;
+constexpr int kTileThreads = 320;
 
 template <int KIND, int BN>
 struct TileShape {
@@ -232,7 +227,9 @@ struct TileShape {
 
 // One block computes one 128 x BN tile over its share of k.  Warp 0 fills the
 // stages, one thread of warp 1 issues the products, warps 2 to 5 bring the
-// scales (MX) and what the epilogue reads, and then read the sums.  Where there
+// scales (MX), and warps 2 to 9 read the sums and store them, eight columns at a
+// time in a loop that is not unrolled: each block runs it once, and fetching
+// straight-line code for 64 columns took longer than the stores (about 3 us).  Where there
 // are too few tiles for the GPU's SMs, a cluster of blocks splits k: each leaves
 // its sums in shared memory and adds up its share of the columns over the
 // cluster, in the order of the ranks, so the result does not depend on timing.
@@ -242,7 +239,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   using S = TileShape<KIND, BN>;
   constexpr bool SYM = EPI == GRAM || EPI == POLY;
   constexpr int kElems = KIND == MX ? 128 : 64;     // values of k in a stage
-  constexpr int kGroups = BN / 16;
+  constexpr int kUnits = BN / 8;
   static_assert(BN <= 128, "");
   static_assert(KIND == F16 || (!R_MN && !C_MN), "8-bit operands are K-major");
   static_assert(!C_MN || BN >= 64, "an MN-major box is 64 wide");
@@ -297,9 +294,10 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     *fail = 1;
     atomicCAS(&g_dense_error, 0, kErrTimeout);
   };
-  // the columns whose sums this block finishes: group g of 16 where g % splits == rank
-  Ahead ahead[kGroups];
-  const int row = r0 + 32 * (warp & 3) + lane;      // of warps 2 to 5
+  // the columns whose sums this warp finishes: units of eight, one in 2 * splits
+  const int row = r0 + 32 * (warp & 3) + lane;
+  const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 2 * p.splits;
+  Ahead<8> ahead;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -368,9 +366,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     if (tc::elect_one()) tc::commit<1>(done);
     __syncwarp();
   } else {
-    const int t = threadIdx.x - 64;   // 0..127
+    const int t = threadIdx.x - 64;   // 0..255
     bool ok = true;
-    if (KIND == MX) {
+    if (KIND == MX && t < 128) {
       const int g1 = kb1 > kb0 ? (kb1 - 1) / 4 + 1 : kb0 / 4;
       int n = 0;
       for (int g = kb0 / 4; g < g1; ++g, ++n) {
@@ -386,9 +384,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         tc::mbar_arrive(sfull + 8 * ss);
       }
     }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      if (g % p.splits == rank) load_ahead<EPI>(p, batch, row, c0 + 16 * g, ahead[g]);
+    if (unit0 < kUnits) load_ahead<EPI, 8>(p, batch, row, c0 + 8 * unit0, ahead);
     ok = ok && tc::mbar_wait(done, 0);
     if (!ok) gave_up();
   }
@@ -396,69 +392,62 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   __syncthreads();
   tc::fence_after();
 
-  // The sums: lane r of the warp's quarter, 16 columns at a time.
+  // The sums: lane r of the warp's quarter, eight columns at a time.
   const bool usable = *fail == 0, some = kb1 > kb0;
   const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
-  if (p.splits == 1) {
-    if (warp >= 2 && usable) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (c0 + 16 * g >= p.cols) break;
-        uint32_t u[16];
-        float v[16];
-        if (some) {
-          tc::tmem_ld16(sums + 16 * g, u);
-          tc::tmem_wait_ld(u);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = some ? __uint_as_float(u[i]) : 0.f;
-        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g], v);
-      }
-    }
-  } else {
-    float* dump = reinterpret_cast<float*>(smem);   // [128][BN + 4], over the stages: no copy is in flight
-    const int rl = 32 * (warp & 3) + lane;
+  const int rl = 32 * (warp & 3) + lane;
+  float* dump = reinterpret_cast<float*>(smem);   // [128][BN + 4], over the stages: no copy is in flight
+  if (p.splits > 1) {
     if (warp >= 2) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        uint32_t u[16];
+#pragma unroll 2
+      for (int u = (warp - 2) >> 2; u < kUnits; u += 2) {
+        uint32_t w[8];
         if (some) {
-          tc::tmem_ld16(sums + 16 * g, u);
-          tc::tmem_wait_ld(u);
+          tc::tmem_ld8(sums + 8 * u, w);
+          tc::tmem_wait_ld8(w);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = 0;
+          for (int i = 0; i < 8; ++i) w[i] = 0;
         }
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 16 * g + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
-      }
-    }
-    tc::cluster_sync();
-    if (warp >= 2 && usable) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (g % p.splits != rank || c0 + 16 * g >= p.cols) continue;
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-#pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) {
-          const uint32_t src = tc::map_rank(ring, s) + (rl * S::kDumpLd + 16 * g) * 4;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 f = tc::ld_cluster4(src + 16 * i);
-            v[4 * i] += f.x;
-            v[4 * i + 1] += f.y;
-            v[4 * i + 2] += f.z;
-            v[4 * i + 3] += f.w;
-          }
-        }
-        finish16<EPI>(p, batch, row, c0 + 16 * g, mirror, ahead[g], v);
+        *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 8 * u + 4) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
     tc::cluster_sync();
   }
+  if (warp >= 2 && usable) {
+#pragma unroll 1
+    for (int u = unit0; u < kUnits; u += step) {
+      const int c = c0 + 8 * u;
+      if (c >= p.cols) break;
+      float v[8];
+      if (p.splits == 1) {
+        uint32_t w[8];
+        if (some) {
+          tc::tmem_ld8(sums + 8 * u, w);
+          tc::tmem_wait_ld8(w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = some ? __uint_as_float(w[i]) : 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        const uint32_t own = ring + (rl * S::kDumpLd + 8 * u) * 4;
+#pragma unroll 2
+        for (int s = 0; s < p.splits; ++s) {
+          const uint32_t src = tc::map_rank(own, s);
+          const float4 f = tc::ld_cluster4(src), g = tc::ld_cluster4(src + 16);
+          v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+          v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
+        }
+      }
+      const Ahead<8> now = ahead;
+      if (u + step < kUnits) load_ahead<EPI, 8>(p, batch, row, c + 8 * step, ahead);
+      finish<EPI, 8>(p, batch, row, c, mirror, now, v);
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) tc::cluster_sync();   // nobody reads this block's sums any more
   tc::fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -723,27 +712,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       bool mirror;
       place(tile, &r0, &c0, &batch, &mirror);
       const int set = n % S::kSets, row = r0 + 32 * (warp & 3) + lane;
-      Ahead ahead[2];
-      uint32_t u[2][16];
-      load_ahead<EPI>(p, batch, row, c0 + 16 * first, ahead[0]);
+      Ahead<16> ahead;
+      uint32_t u[16];
+      load_ahead<EPI, 16>(p, batch, row, c0 + 16 * first, ahead);
       ok = tc::mbar_wait(accfull + 8 * set, (n / S::kSets) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
       if (!ok) break;
       tc::fence_after();
-      tc::tmem_ld16(sums + set * BN + 16 * first, u[0]);
-#pragma unroll
-      for (int i = 0; i < BN / 32; ++i) {
-        const int c = 32 * i + 16 * first;
+      tc::tmem_ld16(sums + set * BN + 16 * first, u);
+#pragma unroll 1
+      for (int c = 16 * first; c < BN; c += 32) {
         if (c0 + c >= p.cols) break;
-        tc::tmem_wait_ld(u[i & 1]);
-        if (i + 1 < BN / 32) {
-          tc::tmem_ld16(sums + set * BN + c + 32, u[(i + 1) & 1]);
-          load_ahead<EPI>(p, batch, row, c0 + c + 32, ahead[(i + 1) & 1]);
-        }
+        tc::tmem_wait_ld(u);
         float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[i & 1][k]);
-        finish16<EPI>(p, batch, row, c0 + c, mirror, ahead[i & 1], v);
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
+        const Ahead<16> now = ahead;
+        if (c + 32 < BN) {
+          tc::tmem_ld16(sums + set * BN + c + 32, u);
+          load_ahead<EPI, 16>(p, batch, row, c0 + c + 32, ahead);
+        }
+        finish<EPI, 16>(p, batch, row, c0 + c, mirror, now, v);
       }
       tc::tmem_drain_ld();
       tc::fence_before();

@@ -243,6 +243,7 @@ def soft_codeword_noalloc(w: torch.Tensor, codebook: torch.Tensor, L: int, k: in
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
 _WIDE = (torch.float32, torch.float16, torch.bfloat16)
 _CODES = (torch.float8_e4m3fn, torch.float8_e5m2)
+_SCALES = (torch.float8_e8m0fnu,)
 _BLOCK = 128
 #: Coefficients of Muon's Newton-Schulz step (the default of orthogonalise and muon_step).
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -336,17 +337,22 @@ def _fp8_quantise(x, block_rows, dtype, minus, layout, st):
     return out + out_t
 
 
-def _scaled(q: torch.Tensor, scale: torch.Tensor, name: str, device) -> int:
-    """Checks codes and their scales; returns the rows that share a scale."""
+def _scaled(q: torch.Tensor, scale: torch.Tensor, name: str, device):
+    """Checks codes and their scales; returns the codes' shape and the call's
+    pointer, type and row stride of the codes, pointer and row stride of the
+    scales, and the rows that share a scale."""
     _matrix(q, name, _CODES, device=device)
-    _matrix(scale, f"scale_{name}", (torch.float8_e8m0fnu,), device=device)
-    if q.numel() and ((q.shape[0] > 1 and q.stride(0) % 16 != 0) or q.data_ptr() % 16 != 0):
+    _matrix(scale, "scale_" + name, _SCALES, device=device)
+    rows, cols = shape = q.shape
+    have = scale.shape
+    blocks = (cols + _BLOCK - 1) // _BLOCK
+    block_rows = 1 if have[0] == rows else _BLOCK
+    if have[1] != blocks or have[0] != (rows + block_rows - 1) // block_rows:
+        raise ValueError(f"scale_{name} must be [{rows}, {blocks}] or [{-(-rows // _BLOCK)}, {blocks}]")
+    ptr, ld = q.data_ptr(), q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    if (ld % 16 or ptr % 16) and rows and cols:
         raise ValueError(f"the rows of {name} must start at multiples of 16 bytes")
-    blocks = -(-q.shape[1] // _BLOCK)
-    for rows in (1, _BLOCK):
-        if tuple(scale.shape) == (-(-q.shape[0] // rows), blocks):
-            return rows
-    raise ValueError(f"scale_{name} must be [{q.shape[0]}, {blocks}] or [{-(-q.shape[0] // _BLOCK)}, {blocks}]")
+    return shape, (ptr, _TYPES[q.dtype], ld, scale.data_ptr(), scale.stride(0) if have[0] > 1 else blocks, block_rows)
 
 
 def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor, alpha: float = 1.0,
@@ -356,29 +362,27 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
     and b [N, K] (e4m3 or e5m2 each) with one scale for each 128 values of K and
     each row or 128 rows, as fp8_quantise gives them.  Sums are in fp32, the
     result (fp32, fp16 or bf16; ``out``, if given, with any row stride) is rounded once."""
-    a_rows = _scaled(a, scale_a, "a", None)
-    b_rows = _scaled(b, scale_b, "b", a.device)
-    (M, K), (N, Kb) = a.shape, b.shape
+    (M, K), args_a = _scaled(a, scale_a, "a", None)
+    device = a.device
+    (N, Kb), args_b = _scaled(b, scale_b, "b", device)
     if K != Kb:
         raise ValueError("a and b must have the same number of columns")
     if out is None:
         if out_dtype not in _WIDE:
             raise TypeError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
     else:
-        _matrix(out, "out", _WIDE, device=a.device)
+        _matrix(out, "out", _WIDE, device=device)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
-    return _call(a.device, stream, _fp8_matmul, a, scale_a, a_rows, b, scale_b, b_rows, alpha, out_dtype, out)
+    return _call(device, stream, _fp8_matmul, args_a, args_b, M, N, K, alpha, out_dtype, out, device)
 
 
-def _fp8_matmul(a, scale_a, a_rows, b, scale_b, b_rows, alpha, out_dtype, out, st):
-    (M, K), N = a.shape, b.shape[0]
+def _fp8_matmul(args_a, args_b, M, N, K, alpha, out_dtype, out, device, st):
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    rc = load().bcjr_fp8_matmul(
-        a.data_ptr(), _TYPES[a.dtype], _ld(a, 16), scale_a.data_ptr(), _ld(scale_a), a_rows, b.data_ptr(),
-        _TYPES[b.dtype], _ld(b, 16), scale_b.data_ptr(), _ld(scale_b), b_rows, M, N, K, alpha, out.data_ptr(),
-        _TYPES[out.dtype], _ld(out), st)
+        out, ld = torch.empty_strided((M, N), (N, 1), dtype=out_dtype, device=device), N
+    else:
+        out_dtype, ld = out.dtype, _ld(out)
+    rc = load().bcjr_fp8_matmul(*args_a, *args_b, M, N, K, alpha, out.data_ptr(), _TYPES[out_dtype], ld, st)
     _check(rc, "bcjr_fp8_matmul")
     return out
 
