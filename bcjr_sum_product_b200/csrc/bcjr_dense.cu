@@ -224,8 +224,18 @@ int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st)
   if (p.cols <= 16) return matmul_tile<16>(r, c, p, nsm, st);
   if (p.cols <= 32) return matmul_tile<32>(r, c, p, nsm, st);
   if (p.cols <= 64) return matmul_tile<64>(r, c, p, nsm, st);
-  if (parts(p.rows, 256) * parts(p.cols, 224) * 4 >= nsm) return matmul_pair<224>(r, c, p, nsm, st);
-  return matmul_tile<128>(r, c, p, nsm, st);
+  // Pairs: the width of tile whose rounds over the GPU take least, from measured times: `block` for 128 values of k
+  // and `end` for what a tile's stores add (256 columns leave room for one set of sums only, so their stores do not
+  // overlap the next tile's products).  8192 x 8192 x 2048: 128 / 224 / 256 columns 160 / 122 / 132 us;
+  // 2048 x 2048 x 8192 (one round of 256, two of 224): 44 / 49 / 32 us.
+  const int64_t pairs = nsm / 2, rows = parts(p.rows, 256), blocks = parts(p.k, 128);
+  const auto cost = [&](int width, double block, double end) {
+    return (double)parts(rows * parts(p.cols, width), pairs) * (blocks * block + end);
+  };
+  const double c128 = cost(128, 0.33, 0.4), c224 = cost(224, 0.435, 0.6), c256 = cost(256, 0.45, 2.2);
+  if (rows * parts(p.cols, 128) * 4 < nsm) return matmul_tile<128>(r, c, p, nsm, st);
+  if (c256 <= c224 && c256 <= c128) return matmul_pair<256>(r, c, p, nsm, st);
+  return c224 <= c128 ? matmul_pair<224>(r, c, p, nsm, st) : matmul_pair<128>(r, c, p, nsm, st);
 }
 
 // ------------------------------------------------------------ Newton-Schulz
@@ -283,7 +293,7 @@ template <int EPI, bool MN>
 int run_sym(const Operand& x, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
   if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN>(x, p, nsm, st);
-  if (t * (t + 1) / 2 * p.batch * 2 < nsm) return sym_tile<64, EPI, MN>(x, p, nsm, st);
+  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN>(x, p, nsm, st);
   return sym_tile<128, EPI, MN>(x, p, nsm, st);
 }
 
@@ -305,7 +315,7 @@ template <int EPI, bool R_MN>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
   if (t2 * parts(p.cols, 256) * p.batch * 4 >= nsm) return iter_pair<256, EPI, R_MN>(r, c, p, nsm, st);
-  if (p.cols <= 64 || t * parts(p.cols, 128) * p.batch * 2 < nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
+  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
   return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
 }
 

@@ -219,10 +219,9 @@ struct TileShape {
   static constexpr int kScaleCols = KIND == MX ? 8 : 0;
   static constexpr int kUsedCols = BN + kScaleStages * kScaleCols;
   static constexpr int kTmemCols = kUsedCols <= 32 ? 32 : kUsedCols <= 64 ? 64 : kUsedCols <= 128 ? 128 : 256;
-  static constexpr int kDumpLd = BN + 4;                       // sums left for the cluster, over the stages
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmem = 1024 + kRing + kScaleStages * kScaleBytes + 256;
-  static_assert(kRowsTile * kDumpLd * 4 <= kRing, "the dump fits the ring");
+  static_assert(kRowsTile * BN * 4 <= kRing, "the sums of a cluster's blocks fit the ring");
 };
 
 // One block computes one 128 x BN tile over its share of k.  Warp 0 fills the
@@ -230,9 +229,9 @@ struct TileShape {
 // scales (MX), and warps 2 to 9 read the sums and store them, eight columns at a
 // time in a loop that is not unrolled: each block runs it once, and fetching
 // straight-line code for 64 columns took longer than the stores (about 3 us).  Where there
-// are too few tiles for the GPU's SMs, a cluster of blocks splits k: each leaves
-// its sums in shared memory and adds up its share of the columns over the
-// cluster, in the order of the ranks, so the result does not depend on timing.
+// are too few tiles for the GPU's SMs, a cluster of blocks splits k: each sends its
+// sums of a unit of columns to the block that finishes it, which adds them up in
+// the order of the ranks, so the result does not depend on timing.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
                                                              const __grid_constant__ CUtensorMap map_c, const Params p) {
@@ -396,8 +395,10 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   const bool usable = *fail == 0, some = kb1 > kb0;
   const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
   const int rl = 32 * (warp & 3) + lane;
-  float* dump = reinterpret_cast<float*>(smem);   // [128][BN + 4], over the stages: no copy is in flight
+  // Unit u is finished by rank u % splits; its sums from rank s lie over the stages of that block (no
+  // copy is in flight there after the first cluster barrier) as [u / splits][s][two halves][128 rows] float4.
   if (p.splits > 1) {
+    tc::cluster_sync();
     if (warp >= 2) {
 #pragma unroll 2
       for (int u = (warp - 2) >> 2; u < kUnits; u += 2) {
@@ -409,8 +410,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = 0;
         }
-        *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dump + rl * S::kDumpLd + 8 * u + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+        const uint32_t to = tc::map_rank(ring + (((u / p.splits) * p.splits + rank) * 256 + rl) * 16, u % p.splits);
+        tc::st_cluster4(to, w[0], w[1], w[2], w[3]);
+        tc::st_cluster4(to + 128 * 16, w[4], w[5], w[6], w[7]);
       }
     }
     tc::cluster_sync();
@@ -432,11 +434,10 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        const uint32_t own = ring + (rl * S::kDumpLd + 8 * u) * 4;
-#pragma unroll 2
+        const float4* from = reinterpret_cast<const float4*>(smem) + (u / p.splits) * p.splits * 256 + rl;
+#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
-          const uint32_t src = tc::map_rank(own, s);
-          const float4 f = tc::ld_cluster4(src), g = tc::ld_cluster4(src + 16);
+          const float4 f = from[256 * s], g = from[256 * s + 128];
           v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
           v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
         }
@@ -446,8 +447,6 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
       finish<EPI, 8>(p, batch, row, c, mirror, now, v);
     }
   }
-  __syncwarp();
-  if (p.splits > 1) tc::cluster_sync();   // nobody reads this block's sums any more
   tc::fence_before();
   __syncthreads();
   if (warp == 1) {
