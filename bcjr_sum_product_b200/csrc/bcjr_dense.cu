@@ -417,13 +417,30 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   return rc;
 }
 
-template <int T>
-int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int64_t tiles, cudaStream_t st) {
-  void (*kern)(Q::QuantParams) = e5m2 ? (row_blocks ? Q::quantise_kernel<T, true, true> : Q::quantise_kernel<T, true, false>)
-                                      : (row_blocks ? Q::quantise_kernel<T, false, true> : Q::quantise_kernel<T, false, false>);
-  kern<<<(unsigned)tiles, Q::kThreads, 0, st>>>(p);
+template <int T, bool PIPE>
+int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> done[4];
+  void (*kern)(Q::QuantParams) =
+      e5m2 ? (row_blocks ? Q::quantise_kernel<T, true, true, PIPE> : Q::quantise_kernel<T, true, false, PIPE>)
+           : (row_blocks ? Q::quantise_kernel<T, false, true, PIPE> : Q::quantise_kernel<T, false, false, PIPE>);
+  const int values = Q::kRows * Q::kThreads * 4;
+  const int smem = PIPE ? values * (T == Q::IN_F32 ? 4 : 2) + (p.minus != nullptr ? values * 4 : 0) : 0;
+  if (PIPE) {
+    const int most = values * (T == Q::IN_F32 ? 8 : 6);
+    if (int rc = allow_smem(reinterpret_cast<const void*>(kern), &done[2 * e5m2 + row_blocks], most)) return rc;
+  }
+  kern<<<grid, Q::kThreads, smem, st>>>(p);
   counted_launch();
   return cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA;
+}
+
+// From four rounds of tiles on, blocks stay (as many as fit the SMs: two, or one where
+// both x and minus are fetched ahead) and fetch ahead.
+template <int T>
+int run_quantise(Q::QuantParams p, bool e5m2, bool row_blocks, int nsm, cudaStream_t st) {
+  if (p.vec && p.tiles > 4 * nsm)
+    return launch_quantise<T, true>(p, e5m2, row_blocks, p.minus != nullptr && T == Q::IN_F32 ? nsm : 2 * nsm, st);
+  return launch_quantise<T, false>(p, e5m2, row_blocks, p.tiles, st);
 }
 
 }  // namespace
@@ -457,11 +474,14 @@ int bcjr_fp8_quantise(const void* x, int x_type, int64_t rows, int64_t cols, int
   p.rows = (int)rows; p.cols = (int)cols; p.tiles_c = (int)tiles_c;
   p.vec = ld_x % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * size_of(x_type)) == 0 &&
           (minus == nullptr || (ld_minus % 4 == 0 && reinterpret_cast<uintptr_t>(minus) % 16 == 0));
+  int nsm = 0;
+  if ((rc = sm_count(&nsm))) return rc;
+  p.tiles = (int)(tiles_r * tiles_c);
   const bool e5m2 = q_type == BCJR_E5M2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (x_type == BCJR_F32) return launch_quantise<Q::IN_F32>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
-  if (x_type == BCJR_F16) return launch_quantise<Q::IN_F16>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
-  return launch_quantise<Q::IN_BF16>(p, e5m2, block_rows == 1, tiles_r * tiles_c, st);
+  if (x_type == BCJR_F32) return run_quantise<Q::IN_F32>(p, e5m2, block_rows == 1, nsm, st);
+  if (x_type == BCJR_F16) return run_quantise<Q::IN_F16>(p, e5m2, block_rows == 1, nsm, st);
+  return run_quantise<Q::IN_BF16>(p, e5m2, block_rows == 1, nsm, st);
 }
 
 int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void* scale_a, int64_t ld_scale_a, int a_block_rows,

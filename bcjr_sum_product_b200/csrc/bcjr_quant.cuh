@@ -51,6 +51,7 @@ struct QuantParams {
   int64_t ld_x, ld_minus, ld_q, ld_s, ld_qt, ld_st;
   int rows, cols, tiles_c;
   int vec;                     // rows of x (and minus) start on 4-element boundaries
+  int tiles;
 };
 
 constexpr int kThreads = 512;
@@ -85,6 +86,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return codes2<E5M2>(a, b) | (codes2<E5M2>(c, d) << 16);
 }
 
+// Asynchronous copy of up to N bytes (8 or 16) to shared memory, zeros behind them.
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+
 // One block takes one 128 x 128 tile of x: warp w the rows 8 w .. 8 w + 7,
 // lane l the columns 4 l .. 4 l + 3, so a tile is read once, in 16-byte loads
 // that are all in flight at once, and stays in registers for both layouts.  The
@@ -93,141 +102,188 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // the columns, or of the tile, meet in shared memory.  The codes of x^T go
 // through shared memory as words of four rows, word index xor (column / 4), so
 // that neither side has bank conflicts.
+// Blocks take tiles in turn.  PIPE: the next tile's values are on their way into
+// shared memory (cp.async, each thread fetching just what it will read, so no
+// barrier guards them) while this one is worked on and stored.
 // ROW_BLOCKS: one scale for each row (or column) and 128 values; else one for the tile.
-template <int T, bool E5M2, bool ROW_BLOCKS>
+template <int T, bool E5M2, bool ROW_BLOCKS, bool PIPE>
 __global__ void __launch_bounds__(kThreads, 2) quantise_kernel(const QuantParams p) {
   constexpr int TOP = E5M2 ? 16 : 9;
-  __shared__ uint32_t most[16][kTile];
+  using X = typename In<T>::type;
+  constexpr int kBytes = 4 * (int)sizeof(X);
+  extern __shared__ __align__(16) uint8_t fetched[];   // PIPE: [8 rows][512 threads] of 4 values of x, then of minus
+  __shared__ alignas(16) uint32_t most[16][kTile];
   __shared__ uint32_t words[kTile][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
-  const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile, c = c0 + 4 * lane;
-  const int live = min(kRows, p.rows - r0);            // rows of this warp, may be <= 0
-  using X = typename In<T>::type;
-  const X* x = static_cast<const X*>(p.x) + (int64_t)r0 * p.ld_x + c;
-  float v[kRows][4];
-  if (live == kRows && c + 4 <= p.cols && p.vec) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) In<T>::get4(x + (int64_t)i * p.ld_x, v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[i][j] = (i < live && c + j < p.cols) ? In<T>::get(x[(int64_t)i * p.ld_x + j]) : 0.f;
-  }
-  if (p.minus != nullptr) {
-    const float* m = p.minus + (int64_t)r0 * p.ld_minus + c;
+  uint8_t* mine = fetched + threadIdx.x * kBytes;
+  uint8_t* mine_minus = fetched + kRows * kThreads * kBytes + threadIdx.x * 16;
+  auto fetch = [&](int tile) {
+    const int r0 = tile / p.tiles_c * kTile + warp * kRows, c = tile % p.tiles_c * kTile + 4 * lane;
+    const int n = max(0, min(4, p.cols - c));        // values of a row
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      float u[4] = {0.f, 0.f, 0.f, 0.f};
-      if (i < live) {
-        if (c + 4 <= p.cols && p.vec) {
-          In<IN_F32>::get4(m + (int64_t)i * p.ld_minus, u);
-        } else {
+      const bool some = r0 + i < p.rows && n > 0;
+      const X* x = static_cast<const X*>(p.x) + (some ? (int64_t)(r0 + i) * p.ld_x + c : 0);
+      copy_async<kBytes>(mine + i * kThreads * kBytes, x, some ? n * (int)sizeof(X) : 0);
+    }
+    if (p.minus != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + j < p.cols) u[j] = m[(int64_t)i * p.ld_minus + j];
+      for (int i = 0; i < kRows; ++i) {
+        const bool some = r0 + i < p.rows && n > 0;
+        const float* m = p.minus + (some ? (int64_t)(r0 + i) * p.ld_minus + c : 0);
+        copy_async<16>(mine_minus + i * kThreads * 16, m, some ? 4 * n : 0);
+      }
+    }
+  };
+  if (PIPE) fetch(blockIdx.x);
+  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const int tr = tile / p.tiles_c, tc = tile % p.tiles_c;
+    const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile, c = c0 + 4 * lane;
+    const int live = min(kRows, p.rows - r0);            // rows of this warp, may be <= 0
+    float v[kRows][4];
+    if (PIPE) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) In<T>::get4(reinterpret_cast<const X*>(mine + i * kThreads * kBytes), v[i]);
+      if (p.minus != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          float u[4];
+          In<IN_F32>::get4(reinterpret_cast<const float*>(mine_minus + i * kThreads * 16), u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = __fsub_rn(v[i][j], u[j]);
         }
       }
+      if (tile + (int)gridDim.x < p.tiles) fetch(tile + gridDim.x);
+    } else {
+      const X* x = static_cast<const X*>(p.x) + (int64_t)r0 * p.ld_x + c;
+      const bool whole = live == kRows && c + 4 <= p.cols && p.vec;
+      if (whole) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = __fsub_rn(v[i][j], u[j]);
-    }
-  }
-
-  uint32_t col[4] = {0, 0, 0, 0};
-  uint32_t rowb[kRows];                                 // row scales as bytes
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    uint32_t b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      b[j] = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
-      col[j] = max(col[j], b[j]);
-    }
-    if (ROW_BLOCKS && p.q != nullptr)
-      rowb[i] = scale_byte<TOP>(__reduce_max_sync(0xFFFFFFFFu, max(max(b[0], b[1]), max(b[2], b[3]))));
-  }
-  uint32_t tile_byte = 0;
-  if (!ROW_BLOCKS) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(max(col[0], col[1]), max(col[2], col[3])));
-    if (lane == 0) most[warp][0] = m;
-    __syncthreads();
-    uint32_t a = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) a = max(a, most[w][0]);
-    tile_byte = scale_byte<TOP>(a);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) rowb[i] = tile_byte;
-  }
-
-  if (p.q != nullptr) {
-    if (ROW_BLOCKS) {
-      if (lane == 0) {
+        for (int i = 0; i < kRows; ++i) In<T>::get4(x + (int64_t)i * p.ld_x, v[i]);
+      } else {
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
-          if (i < live) p.s[(int64_t)(r0 + i) * p.ld_s + tc] = (uint8_t)rowb[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = (i < live && c + j < p.cols) ? In<T>::get(x[(int64_t)i * p.ld_x + j]) : 0.f;
       }
-    } else if (threadIdx.x == 0) {
-      p.s[(int64_t)tr * p.ld_s + tc] = (uint8_t)tile_byte;
+      if (p.minus != nullptr) {
+        const float* m = p.minus + (int64_t)r0 * p.ld_minus + c;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          float u[4] = {0.f, 0.f, 0.f, 0.f};
+          if (whole) {
+            In<IN_F32>::get4(m + (int64_t)i * p.ld_minus, u);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i < live && c + j < p.cols) u[j] = m[(int64_t)i * p.ld_minus + j];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = __fsub_rn(v[i][j], u[j]);
+        }
+      }
     }
-    uint8_t* q = p.q + (int64_t)r0 * p.ld_q + c;
+
+    uint32_t col[4] = {0, 0, 0, 0};
+    uint32_t rowb[kRows];                                 // row scales as bytes
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (i >= live) break;
-      const float f = scale_factor(rowb[i]);
-      const uint32_t w = codes4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
-      if (c + 4 <= p.cols) {
-        *reinterpret_cast<uint32_t*>(q + (int64_t)i * p.ld_q) = w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (c + j < p.cols) q[(int64_t)i * p.ld_q + j] = (uint8_t)(w >> (8 * j));
-      }
-    }
-  }
-
-  if (p.qt != nullptr) {
-    uint32_t colb[4];
-    if (ROW_BLOCKS) {
-      *reinterpret_cast<uint4*>(&most[warp][4 * lane]) = make_uint4(col[0], col[1], col[2], col[3]);
-      __syncthreads();
+      uint32_t b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t a = 0;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) a = max(a, most[w][4 * lane + j]);
-        colb[j] = scale_byte<TOP>(a);
-        if (warp == 0 && c + j < p.cols) p.st[(int64_t)(c + j) * p.ld_st + tr] = (uint8_t)colb[j];
+        b[j] = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
+        col[j] = max(col[j], b[j]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) colb[j] = tile_byte;
-      if (threadIdx.x == 0) p.st[(int64_t)tc * p.ld_st + tr] = (uint8_t)tile_byte;
+      if (ROW_BLOCKS && p.q != nullptr)
+        rowb[i] = scale_byte<TOP>(__reduce_max_sync(0xFFFFFFFFu, max(max(b[0], b[1]), max(b[2], b[3]))));
     }
+    uint32_t tile_byte = 0;
+    if (!ROW_BLOCKS) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(max(col[0], col[1]), max(col[2], col[3])));
+      if (lane == 0) most[warp][0] = m;
+      __syncthreads();
+      uint32_t a = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float f = scale_factor(colb[j]);
+      for (int w = 0; w < 16; ++w) a = max(a, most[w][0]);
+      tile_byte = scale_byte<TOP>(a);
 #pragma unroll
-      for (int i = 0; i < kRows; i += 4)
-        words[4 * lane + j][(warp * (kRows / 4) + i / 4) ^ lane] = codes4<E5M2>(v[i][j] * f, v[i + 1][j] * f, v[i + 2][j] * f, v[i + 3][j] * f);
+      for (int i = 0; i < kRows; ++i) rowb[i] = tile_byte;
     }
-    __syncthreads();
-    const int r = tr * kTile + 4 * lane;             // four rows of x, now columns
+
+    if (p.q != nullptr) {
+      if (ROW_BLOCKS) {
+        if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int cl = warp * kRows + i;
-      if (c0 + cl >= p.cols) break;
-      const uint32_t w = words[cl][lane ^ (cl >> 2)];
-      uint8_t* q = p.qt + (int64_t)(c0 + cl) * p.ld_qt + r;
-      if (r + 4 <= p.rows) {
-        *reinterpret_cast<uint32_t*>(q) = w;
+          for (int i = 0; i < kRows; ++i)
+            if (i < live) p.s[(int64_t)(r0 + i) * p.ld_s + tc] = (uint8_t)rowb[i];
+        }
+      } else if (threadIdx.x == 0) {
+        p.s[(int64_t)tr * p.ld_s + tc] = (uint8_t)tile_byte;
+      }
+      uint8_t* q = p.q + (int64_t)r0 * p.ld_q + c;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (i >= live) break;
+        const float f = scale_factor(rowb[i]);
+        const uint32_t w = codes4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
+        if (c + 4 <= p.cols) {
+          *reinterpret_cast<uint32_t*>(q + (int64_t)i * p.ld_q) = w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (c + j < p.cols) q[(int64_t)i * p.ld_q + j] = (uint8_t)(w >> (8 * j));
+        }
+      }
+    }
+
+    if (p.qt != nullptr) {
+      uint32_t colb[4];
+      if (ROW_BLOCKS) {
+        *reinterpret_cast<uint4*>(&most[warp][4 * lane]) = make_uint4(col[0], col[1], col[2], col[3]);
+        __syncthreads();
+        if (threadIdx.x < kTile) {
+          uint32_t a = 0;
+#pragma unroll
+          for (int w = 0; w < 16; ++w) a = max(a, most[w][threadIdx.x]);
+          a = scale_byte<TOP>(a);
+          most[0][threadIdx.x] = a;    // its own column's: nobody else reads it before the barrier
+          if (c0 + (int)threadIdx.x < p.cols) p.st[(int64_t)(c0 + threadIdx.x) * p.ld_st + tr] = (uint8_t)a;
+        }
+        __syncthreads();
+        const uint4 b = *reinterpret_cast<const uint4*>(&most[0][4 * lane]);
+        colb[0] = b.x; colb[1] = b.y; colb[2] = b.z; colb[3] = b.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (r + j < p.rows) q[j] = (uint8_t)(w >> (8 * j));
+        for (int j = 0; j < 4; ++j) colb[j] = tile_byte;
+        if (threadIdx.x == 0) p.st[(int64_t)tc * p.ld_st + tr] = (uint8_t)tile_byte;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = scale_factor(colb[j]);
+#pragma unroll
+        for (int i = 0; i < kRows; i += 4)
+          words[4 * lane + j][(warp * (kRows / 4) + i / 4) ^ lane] = codes4<E5M2>(v[i][j] * f, v[i + 1][j] * f, v[i + 2][j] * f, v[i + 3][j] * f);
+      }
+      __syncthreads();
+      const int r = tr * kTile + 4 * lane;             // four rows of x, now columns
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int cl = warp * kRows + i;
+        if (c0 + cl >= p.cols) break;
+        const uint32_t w = words[cl][lane ^ (cl >> 2)];
+        uint8_t* q = p.qt + (int64_t)(c0 + cl) * p.ld_qt + r;
+        if (r + 4 <= p.rows) {
+          *reinterpret_cast<uint32_t*>(q) = w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (r + j < p.rows) q[j] = (uint8_t)(w >> (8 * j));
+        }
       }
     }
+    __syncthreads();   // the next tile's sums and words
   }
 }
 
