@@ -40,7 +40,7 @@ static_assert((int)Q::IN_F32 == BCJR_F32 && (int)Q::IN_F16 == BCJR_F16 && (int)Q
 
 constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kMaxMatrix = 65536;   // orthogonalise: rows and columns
-constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxBatch = 32767;    // two planes each, along a grid dimension
 constexpr int kMaxSteps = 64;
 
 // A device or managed pointer of the current device, aligned to `align` bytes.
@@ -158,7 +158,7 @@ int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cl
   return BCJR_OK;
 }
 
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
 int launch_tile(const Operand& r, const Operand& c, const G::Params& p, bool chained, cudaStream_t st) {
   using S = G::TileShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
@@ -166,12 +166,12 @@ int launch_tile(const Operand& r, const Operand& c, const G::Params& p, bool cha
   CUtensorMap mr, mc;
   int rc;
   if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN))) return rc;
-  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI>;
+  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI, PL>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   return launch(kern, (int64_t)p.tiles * p.splits, p.batch, G::kTileThreads, S::kSmem, p.splits, chained, mr, mc, p, st);
 }
 
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
 int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm, bool chained, cudaStream_t st) {
   using S = G::PairShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
@@ -179,7 +179,7 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   CUtensorMap mr, mc;
   int rc;
   if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN / 2))) return rc;
-  auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI>;
+  auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI, PL>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
   // The pairs that run together work on neighbouring columns of all of R, which then has to stay in
@@ -206,7 +206,7 @@ int matmul_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)tiles;
   p.splits = splits_for(tiles, parts(p.k, 128), nsm);
-  return launch_tile<G::MX, BN, false, false, G::OUT>(r, c, p, false, st);
+  return launch_tile<G::MX, BN, false, false, G::OUT, 1>(r, c, p, false, st);
 }
 template <int BN>
 int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
@@ -214,7 +214,7 @@ int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   if (tiles > INT32_MAX / 2) return BCJR_ERR_UNSUPPORTED;
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)tiles;
-  return launch_pair<G::MX, BN, false, false, G::OUT>(r, c, p, nsm, false, st);
+  return launch_pair<G::MX, BN, false, false, G::OUT, 1>(r, c, p, nsm, false, st);
 }
 
 int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
@@ -275,48 +275,48 @@ int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps)
 }
 
 // P = X X^T (or X^T X), B = a I + b P + c P^2: x against itself, tiles up to the diagonal.
-template <int BN, int EPI, bool MN>
+template <int BN, int EPI, bool MN, int PL>
 int sym_tile(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile);
   p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64), nsm);
-  return launch_tile<G::F16, BN, MN, MN, EPI>(x, x, p, true, st);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL > 1 ? 3 : 1), nsm);
+  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, x, p, true, st);
 }
-template <int BN, int EPI, bool MN>
+template <int BN, int EPI, bool MN, int PL>
 int sym_pair(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, 2 * G::kRowsTile);
   p.tiles_r = (int)t;
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
-  return launch_pair<G::F16, BN, MN, MN, EPI>(x, x, p, nsm, true, st);
+  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, x, p, nsm, true, st);
 }
-template <int EPI, bool MN>
+template <int EPI, bool MN, int PL>
 int run_sym(const Operand& x, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN>(x, p, nsm, st);
-  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN>(x, p, nsm, st);
-  return sym_tile<128, EPI, MN>(x, p, nsm, st);
+  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, p, nsm, st);
+  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN, PL>(x, p, nsm, st);
+  return sym_tile<128, EPI, MN, PL>(x, p, nsm, st);
 }
 
 // X' = B X (or X B).
-template <int BN, int EPI, bool R_MN>
+template <int BN, int EPI, bool R_MN, int PL>
 int iter_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64), nsm);
-  return launch_tile<G::F16, BN, R_MN, false, EPI>(r, c, p, true, st);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL > 1 ? 3 : 1), nsm);
+  return launch_tile<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, true, st);
 }
-template <int BN, int EPI, bool R_MN>
+template <int BN, int EPI, bool R_MN, int PL>
 int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  return launch_pair<G::F16, BN, R_MN, false, EPI>(r, c, p, nsm, true, st);
+  return launch_pair<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, nsm, true, st);
 }
-template <int EPI, bool R_MN>
+template <int EPI, bool R_MN, int PL>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (t2 * parts(p.cols, 256) * p.batch * 4 >= nsm) return iter_pair<256, EPI, R_MN>(r, c, p, nsm, st);
-  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
-  return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
+  if (t2 * parts(p.cols, 256) * p.batch * 4 >= nsm) return iter_pair<256, EPI, R_MN, PL>(r, c, p, nsm, st);
+  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN, PL>(r, c, p, nsm, st);
+  return iter_tile<128, EPI, R_MN, PL>(r, c, p, nsm, st);
 }
 
 template <int T>
@@ -326,8 +326,9 @@ void launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
   counted_launch(2);
 }
 
-// The whole iteration; `last` holds the epilogue of the last product (out, its
+// The whole iteration, with iterates of PL planes; `last` holds the epilogue of the last product (out, its
 // layout and type, the weights' factors) and says which by `epi`.
+template <int PL>
 int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi,
                       const G::Params& last, cudaStream_t st) {
   int nsm = 0;
@@ -343,10 +344,10 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   double* partial;
   auto layout = [&](Arena& ar) {
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
-    x0 = ar.take<__half>((size_t)(sh.batch * nx));
-    x1 = ar.take<__half>((size_t)(sh.batch * nx));
-    pp = ar.take<__half>((size_t)(sh.batch * np));
-    bb = ar.take<__half>((size_t)(sh.batch * np));
+    x0 = ar.take<__half>((size_t)(sh.batch * PL * nx));
+    x1 = ar.take<__half>((size_t)(sh.batch * PL * nx));
+    pp = ar.take<__half>((size_t)(sh.batch * PL * np));
+    bb = ar.take<__half>((size_t)(sh.batch * PL * np));
   };
   Arena sizing;
   layout(sizing);
@@ -359,7 +360,9 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   u.partial = partial;
   u.x = x0;
   u.ld_x = ld_x;
-  u.batch_x = nx;
+  u.batch_x = PL * nx;
+  u.plane_x = nx;
+  u.planes = PL;
   u.rows = (int)sh.rows;
   u.cols = (int)sh.cols;
   u.scale = G::kIterScale;
@@ -375,28 +378,30 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     const float* co = coeffs != nullptr ? coeffs + 3 * s : kMuonCoeffs;
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
-    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch, nx};
+    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * PL, nx};
     G::Params p{};
     p.rows = p.cols = (int)m;
     p.k = (int)(tall ? sh.rows : sh.cols);
     p.batch = (int)sh.batch;
     p.out = pp;
     p.ld_out = ld_p;
-    p.batch_out = np;
-    rc = tall ? run_sym<G::GRAM, true>(x, p, nsm, st) : run_sym<G::GRAM, false>(x, p, nsm, st);
+    p.batch_out = PL * np;
+    p.plane_out = np;
+    rc = tall ? run_sym<G::GRAM, true, PL>(x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, p, nsm, st);
     if (rc) break;
-    const Operand gram{pp, m, m, ld_p, sh.batch, np};
+    const Operand gram{pp, m, m, ld_p, sh.batch * PL, np};
     p.k = (int)m;
     p.out = bb;
     p.x = pp;
     p.ld_x = ld_p;
-    p.batch_x = np;
+    p.batch_x = PL * np;
+    p.plane_x = np;
     p.fa = co[0];
     p.fb = co[1];
     p.fc = co[2];
-    if ((rc = run_sym<G::POLY, false>(gram, p, nsm, st))) break;
+    if ((rc = run_sym<G::POLY, false, PL>(gram, p, nsm, st))) break;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
-    const Operand poly{bb, m, m, ld_p, sh.batch, np};
+    const Operand poly{bb, m, m, ld_p, sh.batch * PL, np};
     const bool end = s + 1 == steps;
     G::Params q = end ? last : G::Params{};
     q.rows = (int)sh.cols;
@@ -406,10 +411,17 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     if (!end) {
       q.out = x1;
       q.ld_out = ld_x;
-      q.batch_out = nx;
+      q.batch_out = PL * nx;
+      q.plane_out = nx;
     }
-#define BCJR_ITER(E) (tall ? run_iter<E, false>(poly, x, q, nsm, st) : run_iter<E, true>(x, poly, q, nsm, st))
-    rc = !end ? BCJR_ITER(G::ITER) : epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
+#define BCJR_ITER(E) (tall ? run_iter<E, false, PL>(poly, x, q, nsm, st) : run_iter<E, true, PL>(x, poly, q, nsm, st))
+    if (!end) {
+      rc = BCJR_ITER(G::ITER);
+    } else if constexpr (PL == 1) {
+      rc = epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
+    } else {
+      rc = BCJR_ITER(G::LAST);
+    }
 #undef BCJR_ITER
     std::swap(x0, x1);
   }
@@ -532,7 +544,10 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
   u.g = g; u.ld_g = ld_g; u.batch_g = batch_stride_g; u.eps = eps;
   G::Params last{};
   last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
-  return run_newton_schulz(sh, u, g_type, steps, coeffs, G::LAST, last, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // one plane of 11 bits leaves less than bf16's own rounding; fp16 shows more
+  return out_type == BCJR_BF16 ? run_newton_schulz<1>(sh, u, g_type, steps, coeffs, G::LAST, last, st)
+                               : run_newton_schulz<2>(sh, u, g_type, steps, coeffs, G::LAST, last, st);
 }
 
 int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad, float* momentum,
@@ -553,7 +568,7 @@ int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int6
   last.out = w; last.ld_out = ld_w;
   last.keep = (float)(1.0 - (double)lr * (double)weight_decay);
   last.rate = (float)((double)lr * (double)scale);
-  return run_newton_schulz(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
+  return run_newton_schulz<1>(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

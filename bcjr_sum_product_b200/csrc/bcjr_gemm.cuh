@@ -48,7 +48,10 @@ enum Epilogue {
 };
 enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 
-// The iterates are kept as fp16(2^12 x): |x| <= 16 stays finite, and values are
+// The iterates are kept as fp16(2^12 x), or for outputs of more than 8 bits as the
+// sum of two such planes (the value and what its rounding left: 22 bits), whose
+// product takes three passes over k: R0 C0 + R0 C1 + R1 C0 (PL below: one plane or
+// two).  2^12:: |x| <= 16 stays finite, and values are
 // rounded to 11 bits down to 2^-26 instead of 2^-14 (the entries of a large
 // matrix of norm 1 are that small).
 constexpr float kIterScale = 4096.f;
@@ -71,6 +74,7 @@ struct Params {
   const __half* x;           // P (POLY), laid out as D
   int64_t ld_out, ld_x;
   int64_t batch_out, batch_x;
+  int64_t plane_out, plane_x;   // PL = 2: from one plane to the other
   int out_type;
   float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
@@ -96,23 +100,25 @@ __device__ __forceinline__ void store_columns(void* out, int64_t at, int64_t ld,
 
 // What the end of W columns of a row reads, loaded ahead: W entries of row r of P
 // (symmetric, so they lie side by side; ld_x is a multiple of 8).
-template <int W>
+template <int W, int PL>
 struct Ahead {
-  uint4 h[W / 8];
+  uint4 h[PL][W / 8];
 };
-template <int EPI, int W>
-__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W>& a) {
+template <int EPI, int W, int PL>
+__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W, PL>& a) {
   if (EPI == POLY && r < p.rows) {
     const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x + c0;
 #pragma unroll
-    for (int i = 0; i < W / 8; ++i)
-      a.h[i] = c0 + 8 * i < p.cols ? *reinterpret_cast<const uint4*>(x + 8 * i) : make_uint4(0, 0, 0, 0);
+    for (int l = 0; l < PL; ++l)
+#pragma unroll
+      for (int i = 0; i < W / 8; ++i)
+        a.h[l][i] = c0 + 8 * i < p.cols ? *reinterpret_cast<const uint4*>(x + l * p.plane_x + 8 * i) : make_uint4(0, 0, 0, 0);
   }
 }
 
 // Stores columns c0..c0+W-1 (as far as they exist) of row r.
-template <int EPI, int W>
-__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead<W>& a,
+template <int EPI, int W, int PL>
+__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead<W, PL>& a,
                                        float (&v)[W]) {
   if (r >= p.rows) return;
   const int n = p.cols - c0;
@@ -126,28 +132,36 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
     else store_columns<OUT_BF16, W>(p.out, at, p.ld_out, n, v);
   } else if constexpr (EPI == GRAM || EPI == POLY || EPI == ITER) {
     if constexpr (EPI == POLY) {
-      const __half* x = reinterpret_cast<const __half*>(a.h);
+      const __half* x = reinterpret_cast<const __half*>(a.h);   // W values, then what they left
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        v[i] = fmaf(p.fb, __half2float(x[i]), p.fc * v[i]);
+        const float pv = PL > 1 ? __half2float(x[i]) + __half2float(x[(PL - 1) * W + i]) : __half2float(x[i]);
+        v[i] = fmaf(p.fb, pv, p.fc * v[i]);
         if (c0 + i == r) v[i] += p.fa * kIterScale;
       }
     }
-    alignas(16) __half h[W];
+    __half* const o = static_cast<__half*>(p.out) + at;
+    __half* const m = static_cast<__half*>(p.out) + batch * p.batch_out + (int64_t)r * p.ld_out + c0;   // 16-byte aligned
 #pragma unroll
-    for (int i = 0; i < W; ++i) h[i] = __float2half_rn(v[i]);
-    __half* o = static_cast<__half*>(p.out) + at;
+    for (int plane = 0; plane < PL; ++plane) {
+      alignas(16) __half h[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (i < n) *o = h[i];
-      o += p.ld_out;
-    }
-    if (EPI != ITER && mirror) {
-      __half* m = static_cast<__half*>(p.out) + batch * p.batch_out + (int64_t)r * p.ld_out + c0;   // 16-byte aligned
+      for (int i = 0; i < W; ++i) {
+        h[i] = __float2half_rn(v[i]);
+        if (PL > 1) v[i] -= __half2float(h[i]);
+      }
+      __half* to = o + plane * p.plane_out;
 #pragma unroll
-      for (int j = 0; j < W / 8; ++j) {
-        // whole groups of 8 stay inside the row's room (ld_out is the columns rounded up to 8)
-        if (8 * j < n) reinterpret_cast<uint4*>(m)[j] = reinterpret_cast<const uint4*>(h)[j];
+      for (int i = 0; i < W; ++i) {
+        if (i < n) *to = h[i];
+        to += p.ld_out;
+      }
+      if (EPI != ITER && mirror) {
+#pragma unroll
+        for (int j = 0; j < W / 8; ++j) {
+          // whole groups of 8 stay inside the row's room (ld_out is the columns rounded up to 8)
+          if (8 * j < n) reinterpret_cast<uint4*>(m + plane * p.plane_out)[j] = reinterpret_cast<const uint4*>(h)[j];
+        }
       }
     }
   } else {   // STEP
@@ -177,6 +191,16 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int
     }
   }
   return w;
+}
+
+// Place of block kb of k: operands of two planes are gone through three times.  The
+// first value of k, the third coordinates of R and C in their maps.
+template <int KIND, int PL>
+__device__ __forceinline__ void block_place(int kb, int blocks, int batch, int* k, int* zr, int* zc) {
+  const int pass = PL == 1 || kb < blocks ? 0 : kb < 2 * blocks ? 1 : 2;
+  *k = (kb - pass * blocks) * (KIND == MX ? 128 : 64);
+  *zr = batch * PL + (pass == 2 ? 1 : 0);
+  *zc = batch * PL + (pass == 1 ? 1 : 0);
 }
 
 // Tile t of a symmetric product of TR-row and TC-column tiles: row tile j has the
@@ -232,7 +256,7 @@ struct TileShape {
 // are too few tiles for the GPU's SMs, a cluster of blocks splits k: each sends its
 // sums of a unit of columns to the block that finishes it, which adds them up in
 // the order of the ranks, so the result does not depend on timing.
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
 __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
                                                              const __grid_constant__ CUtensorMap map_c, const Params p) {
   using S = TileShape<KIND, BN>;
@@ -265,7 +289,8 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   }
   const int r0 = tr * kRowsTile, c0 = tcn * BN;
   const int blocks = (p.k + kElems - 1) / kElems;
-  const int kb0 = (int)((int64_t)blocks * rank / p.splits), kb1 = (int)((int64_t)blocks * (rank + 1) / p.splits);
+  const int total = PL > 1 ? 3 * blocks : blocks;
+  const int kb0 = (int)((int64_t)total * rank / p.splits), kb1 = (int)((int64_t)total * (rank + 1) / p.splits);
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_r);
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   // the columns whose sums this warp finishes: units of eight, one in 2 * splits
   const int row = r0 + 32 * (warp & 3) + lane;
   const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 2 * p.splits;
-  Ahead<8> ahead;
+  Ahead<8, PL> ahead;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -309,18 +334,20 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         }
         const uint32_t dst = ring + s * S::kStageBytes, bar = full + 8 * s;
         tc::mbar_expect(bar, S::kStageBytes);
+        int k, zr, zc;
+        block_place<KIND, PL>(kb, blocks, batch, &k, &zr, &zc);
         if (R_MN) {
-          tc::tma_load3(dst, &map_r, r0, kb * kElems, batch, bar);
-          tc::tma_load3(dst + 8192, &map_r, r0 + 64, kb * kElems, batch, bar);
+          tc::tma_load3(dst, &map_r, r0, k, zr, bar);
+          tc::tma_load3(dst + 8192, &map_r, r0 + 64, k, zr, bar);
         } else {
-          tc::tma_load3(dst, &map_r, kb * kElems, r0, batch, bar);
+          tc::tma_load3(dst, &map_r, k, r0, zr, bar);
         }
         if (C_MN) {
 #pragma unroll
           for (int i = 0; i < BN / 64; ++i)
-            tc::tma_load3(dst + kStageBytesR + 8192 * i, &map_c, c0 + 64 * i, kb * kElems, batch, bar);
+            tc::tma_load3(dst + kStageBytesR + 8192 * i, &map_c, c0 + 64 * i, k, zc, bar);
         } else {
-          tc::tma_load3(dst + kStageBytesR, &map_c, kb * kElems, c0, batch, bar);
+          tc::tma_load3(dst + kStageBytesR, &map_c, k, c0, zc, bar);
         }
         ++issued;
       }
@@ -383,7 +410,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         tc::mbar_arrive(sfull + 8 * ss);
       }
     }
-    if (unit0 < kUnits) load_ahead<EPI, 8>(p, batch, row, c0 + 8 * unit0, ahead);
+    if (unit0 < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c0 + 8 * unit0, ahead);
     ok = ok && tc::mbar_wait(done, 0);
     if (!ok) gave_up();
   }
@@ -442,9 +469,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
           v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
         }
       }
-      const Ahead<8> now = ahead;
-      if (u + step < kUnits) load_ahead<EPI, 8>(p, batch, row, c + 8 * step, ahead);
-      finish<EPI, 8>(p, batch, row, c, mirror, now, v);
+      const Ahead<8, PL> now = ahead;
+      if (u + step < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c + 8 * step, ahead);
+      finish<EPI, 8, PL>(p, batch, row, c, mirror, now, v);
     }
   }
   tc::fence_before();
@@ -486,7 +513,7 @@ struct PairShape {
 // tile while the next is computed.  Warps 2 and 3 bring the scales.  A stage holds
 // two blocks of k, since every commit (the hand-back of a stage) makes the tensor
 // cores pause: about 0.13 us each, measured.
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ CUtensorMap map_r,
                                                                 const __grid_constant__ CUtensorMap map_c, const Params p) {
   using S = PairShape<KIND, BN>;
@@ -511,6 +538,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int all = p.tiles * p.batch;
   const int blocks = (p.k + kElems - 1) / kElems;   // > 0
+  const int total = PL > 1 ? 3 * blocks : blocks;
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_r);
@@ -566,27 +594,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         bool mirror;
         place(tile, &r0, &c0, &batch, &mirror);
         const int ch = c0 + (int)rank * kHalf;
-        for (int kb = 0; kb < blocks; kb += S::kSub, ++it) {
-          const int s = it % S::kStages, n = min(S::kSub, blocks - kb);
+        for (int kb = 0; kb < total; kb += S::kSub, ++it) {
+          const int s = it % S::kStages, n = min(S::kSub, total - kb);
           ok = tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
           if (!ok) break;
           const uint32_t bar = tc::map_rank(full + 8 * s, 0);
           if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * n * S::kSubBytes);   // both blocks' bytes
           for (int j = 0; j < n; ++j) {
             const uint32_t dst = ring + s * S::kStageBytes + j * S::kSubBytes;
-            const int k = (kb + j) * kElems;
+            int k, zr, zc;
+            block_place<KIND, PL>(kb + j, blocks, batch, &k, &zr, &zc);
             if (R_MN) {
-              tc::tma_load3_pair(dst, &map_r, r0, k, batch, bar);
-              tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, k, batch, bar);
+              tc::tma_load3_pair(dst, &map_r, r0, k, zr, bar);
+              tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, k, zr, bar);
             } else {
-              tc::tma_load3_pair(dst, &map_r, k, r0, batch, bar);
+              tc::tma_load3_pair(dst, &map_r, k, r0, zr, bar);
             }
             if (C_MN) {
 #pragma unroll
               for (int i = 0; i < kHalf / 64; ++i)
-                tc::tma_load3_pair(dst + kStageBytesR + 8192 * i, &map_c, ch + 64 * i, k, batch, bar);
+                tc::tma_load3_pair(dst + kStageBytesR + 8192 * i, &map_c, ch + 64 * i, k, zc, bar);
             } else {
-              tc::tma_load3_pair(dst + kStageBytesR, &map_c, k, ch, batch, bar);
+              tc::tma_load3_pair(dst + kStageBytesR, &map_c, k, ch, zc, bar);
             }
           }
         }
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = acc + set * BN;
-        for (int kb = 0; kb < blocks; kb += S::kSub, ++it) {
+        for (int kb = 0; kb < total; kb += S::kSub, ++it) {
           const int s = it % S::kStages;
           ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1));
           if (!ok) break;
@@ -635,7 +664,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
           if (tc::elect_one()) {
 #pragma unroll
             for (int j = 0; j < S::kSub; ++j) {
-              if (kb + j < blocks) {
+              if (kb + j < total) {
                 const uint32_t a = ring + s * S::kStageBytes + j * S::kSubBytes;
                 stage_products<2, KIND, R_MN, C_MN>(d, a, a + kStageBytesR,
                                                     KIND == MX ? tc::idesc_mx_id(idesc, (kb + j) & 3) : idesc, ts, kb + j > 0);
@@ -711,9 +740,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       bool mirror;
       place(tile, &r0, &c0, &batch, &mirror);
       const int set = n % S::kSets, row = r0 + 32 * (warp & 3) + lane;
-      Ahead<16> ahead;
+      Ahead<16, PL> ahead;
       uint32_t u[16];
-      load_ahead<EPI, 16>(p, batch, row, c0 + 16 * first, ahead);
+      load_ahead<EPI, 16, PL>(p, batch, row, c0 + 16 * first, ahead);
       ok = tc::mbar_wait(accfull + 8 * set, (n / S::kSets) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
       if (!ok) break;
@@ -726,12 +755,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         float v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
-        const Ahead<16> now = ahead;
+        const Ahead<16, PL> now = ahead;
         if (c + 32 < BN) {
           tc::tmem_ld16(sums + set * BN + c + 32, u);
-          load_ahead<EPI, 16>(p, batch, row, c0 + c + 32, ahead);
+          load_ahead<EPI, 16, PL>(p, batch, row, c0 + c + 32, ahead);
         }
-        finish<EPI, 16>(p, batch, row, c0 + c, mirror, now, v);
+        finish<EPI, 16, PL>(p, batch, row, c0 + c, mirror, now, v);
       }
       tc::tmem_drain_ld();
       tc::fence_before();

@@ -296,10 +296,12 @@ struct UpdateParams {
   const void* g;
   float* momentum;         // or null: the update is g itself
   double* partial;         // [batch][parts]
-  __half* x;               // [batch][rows][ld_x]
+  __half* x;               // [batch][planes][rows][ld_x]
   int64_t ld_g, batch_g, ld_m, ld_x, batch_x;
   int rows, cols, parts;
   int vec;                 // rows of g and momentum start on 4-element boundaries
+  int planes;              // 2: what the rounding of the first plane left in a second
+  int64_t plane_x;
   float mu;
   int nesterov;
   float eps, scale;
@@ -407,12 +409,14 @@ __global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParam
     for (int j = 0; j < 4; ++j) {
       const int at = c + 128 * j;
       if (at >= p.cols) break;
-      alignas(8) __half h[4];
+      alignas(8) __half h[4], l[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float v = mp == nullptr ? u[4 * j + k] : update_of(p, u[4 * j + k], m[4 * j + k]);
-        h[k] = __float2half_rn(v * f);
+        const float v = (mp == nullptr ? u[4 * j + k] : update_of(p, u[4 * j + k], m[4 * j + k])) * f;
+        h[k] = __float2half_rn(v);
+        l[k] = __float2half_rn(v - __half2float(h[k]));
       }
+      if (p.planes > 1) *reinterpret_cast<uint2*>(o + p.plane_x + at) = *reinterpret_cast<const uint2*>(l);
       // rows of x have room for whole groups of 8
       *reinterpret_cast<uint2*>(o + at) = *reinterpret_cast<const uint2*>(h);
     }

@@ -403,8 +403,9 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = 
                   out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """bcjr_orthogonalise: Newton-Schulz orthogonalisation of a matrix or a batch of
     matrices ``g`` ([rows, cols] or [batch, rows, cols]; fp32, fp16, bf16) after
-    division by its Frobenius norm + eps; fp16 or bf16 of the shape of g.  Products
-    take fp16 operands and sum in fp32.  ``coeffs`` is (a, b, c), or one such triple
+    division by its Frobenius norm + eps; bf16 or fp16 of the shape of g.
+    Products sum in fp32; their operands have 11 bits for a bf16 result and 22 (at
+    three times the work) for an fp16 one.  ``coeffs`` is (a, b, c), or one such triple
     for each step; the default is Muon's."""
     if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
         raise ValueError("g must be a matrix or a batch of matrices")

@@ -265,14 +265,16 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * X_0 = G / (||G||_F + eps) and, for each of `steps` steps and its coefficients
  * (a, b, c), X <- a X + (b A + c A^2) X where A = X X^T (X^T X from the right
  * when rows > cols), out is the last X: G with its singular values moved
- * towards 1.  Iterates and Gram matrices are held in fp16 scaled by 2^12
- * (11 bits of mantissa; products summed in fp32), so out, fp16 or bf16, is
- * within about 1e-3 of the exact iteration in the 2-norm.
+ * towards 1.  Products sum in fp32.  For a bf16 out their operands, the iterates
+ * and Gram matrices, are fp16 scaled by 2^12 (11 bits), which keeps out within
+ * about 1.5e-3 of the exact iteration in the 2-norm, less than its own rounding;
+ * for an fp16 out they are pairs of such values (22 bits, three times the
+ * products), and out is within about 2e-5 before it is rounded.
  *   g       [batch][rows][cols]  fp32, fp16 or bf16 (input)
  *   coeffs  [steps][3]           HOST pointer, read during the call, or NULL
  *                                for Muon's (3.4445, -4.7750, 2.0315)
  *   out     [batch][rows][cols]  fp16 or bf16 (output)
- * rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.  Coefficients that drive a
+ * batch <= 32767, rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.  Coefficients that drive a
  * singular value of [0, 1] above 2 are BCJR_ERR_INVALID_ARG.  A matrix of zeros
  * gives zeros (eps > 0); NaN or infinities make that matrix NaN.
  */
@@ -286,8 +288,8 @@ BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_
  *   u         = grad + mu momentum (nesterov != 0), or momentum
  *   w        <- (1 - lr weight_decay) w - lr scale orthogonalise(u)
  *   w, momentum  [rows][cols] fp32 (updated), grad [rows][cols] fp32, fp16 or bf16
- * steps, coeffs and eps as in bcjr_orthogonalise; lr, mu, weight_decay and scale
- * finite.
+ * steps, coeffs and eps as in bcjr_orthogonalise, operands as for its bf16
+ * output; lr, mu, weight_decay and scale finite.
  */
 BCJR_API int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad,
                             float* momentum, int64_t ld_momentum, int64_t rows, int64_t cols, float lr, float mu,

@@ -80,6 +80,39 @@ def test_quantise_extreme_blocks():
     check_codes(q, s, x, 128, E4M3)
 
 
+@pytest.mark.parametrize("rows,cols,x_dtype,minus", [(3200, 3205, torch.float32, True), (1000, 9996, torch.bfloat16, False),
+                                                     (9999, 1002, torch.float32, False), (2500, 4000, torch.bfloat16, True)])
+def test_quantise_many_tiles(rows, cols, x_dtype, minus):
+    """Matrices of many tiles take a path of their own; it has to give the codes that
+    their parts give, with row starts on 16-byte boundaries and off them."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    room = torch.randn(rows, cols + 15, generator=g, device=DEV).to(x_dtype)
+    room = torch.nn.functional.pad(room, (0, -room.shape[1] % 8))
+    m = torch.randn(rows, cols, generator=g, device=DEV) if minus else None
+    for at in (0, 3, 8):
+        x = room[:, at:at + cols]
+        whole = lib.fp8_quantise(x, 1, E4M3, minus=m, layout="both")
+        blocks = lib.fp8_quantise(x, 128, E4M3, minus=m, layout="both")
+        for r in range(0, rows, 1280):                       # 128-row borders
+            sub, msub = x[r:r + 1280, :512], None if m is None else m[r:r + 1280, :512]
+            q, s, qt, st = lib.fp8_quantise(sub, 1, E4M3, minus=msub, layout="both")
+            assert torch.equal(q.view(torch.uint8), whole[0][r:r + 1280, :512].view(torch.uint8))
+            assert torch.equal(s.view(torch.uint8), whole[1][r:r + 1280, :4].view(torch.uint8))
+            assert torch.equal(qt.view(torch.uint8), whole[2][:512, r:r + 1280].view(torch.uint8))
+            assert torch.equal(st.view(torch.uint8), whole[3][:512, r // 128:(r + 1280) // 128].view(torch.uint8))
+            q, s, qt, st = lib.fp8_quantise(sub, 128, E4M3, minus=msub, layout="both")
+            assert torch.equal(q.view(torch.uint8), blocks[0][r:r + 1280, :512].view(torch.uint8))
+            assert torch.equal(qt.view(torch.uint8), blocks[2][:512, r:r + 1280].view(torch.uint8))
+            assert torch.equal(s.view(torch.uint8), blocks[1][r // 128:r // 128 + 10, :4].view(torch.uint8))
+        finished()
+        # the ragged corner against the definition
+        r, c = rows // 128 * 128, cols // 128 * 128
+        v = (x[r:, c:].float() if m is None else x[r:, c:].float() - m[r:, c:]).cpu()
+        check_codes(whole[0][r:, c:], whole[1][r:, c // 128:], v, 1, E4M3)
+        check_codes(whole[2][c:, r:], whole[3][c:, r // 128:], v.t(), 1, E4M3)
+        check_codes(blocks[0][r:, c:], blocks[1][r // 128:, c // 128:], v, 128, E4M3)
+
+
 def test_quantise_strided_and_unaligned_inputs():
     room = randn(140, 300, seed=5).to(DEV)
     for view in (room[:, 1:270], room[3:, 4:204], room.to(torch.bfloat16)[1::2, 3:132]):
@@ -225,12 +258,30 @@ def test_orthogonalise(rows, cols, dtype):
     check_orthogonal(out, g)
 
 
-@pytest.mark.parametrize("rows,cols", [(512, 1536), (1536, 512), (700, 2100)])
+@pytest.mark.parametrize("rows,cols", [(512, 1536), (1536, 512), (700, 2100), (1300, 2700), (2700, 1300)])
 def test_orthogonalise_large(rows, cols):
     g = randn(rows, cols, seed=21)
-    out = lib.orthogonalise(g.to(DEV), out_dtype=torch.float16)
+    out = lib.orthogonalise(g.to(DEV))
     finished()
     check_orthogonal(out, g)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 40), (30, 30), (130, 333), (333, 130), (512, 700), (1300, 1400), (1500, 1300)])
+def test_orthogonalise_two_planes(rows, cols):
+    """An fp16 result: operands of 22 bits.  Three roundings a step of at most 2^-22, and
+    sums of n terms in fp32 of at most (n / 16 + 16) whole steps of sums of absolute
+    values, which the norms bound by sqrt(n) times the result; the smallest singular
+    values of a square matrix grow 485 times while the norm grows sqrt(rank), so errors
+    grow at most 485 / sqrt(rank) times against the result."""
+    g = randn(rows, cols, seed=rows + 2 * cols)
+    out = lib.orthogonalise(g.to(DEV), out_dtype=torch.float16)
+    finished()
+    want = ref.newton_schulz(g)
+    rel = float(torch.linalg.vector_norm(out.cpu().double() - want) / torch.linalg.vector_norm(want))
+    n = max(rows, cols)
+    assert rel <= 485 / math.sqrt(min(rows, cols)) * (15 * 2.0 ** -22 + 15 * (n / 16 + 16) * 2.0 ** -23) + HALF_STEP[torch.float16]
+    # and, since those are worst cases: closer than operands of 11 bits could come (3e-4 or more)
+    assert rel <= 2.5e-4
 
 
 def test_orthogonalise_batch_strides_and_zeros():
