@@ -87,6 +87,7 @@ CODEBOOK_SEED = 0
 WEIGHT_SEED = 1
 GRAD_SEED = 2
 SUBSET_SEED = 3
+ACTIVATION_SEED = 4
 
 
 def codebook(L: int, V: int, seed: int = CODEBOOK_SEED) -> torch.Tensor:
