@@ -181,7 +181,7 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int
   uint32_t w = 0x7F7F7F7Fu;
   if (row < rows) {
     const uint8_t* q = s + (int64_t)(row >> shift) * ld + 4 * g;
-    const int n = blocks - 4 * g;
+    const int n = blocks - 4 * g;                     // may be <= 0
     if (n >= 4 && (reinterpret_cast<uintptr_t>(q) & 3) == 0) {
       w = *reinterpret_cast<const uint32_t*>(q);
     } else {
@@ -190,6 +190,20 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int
         if (i < n) w = (w & ~(0xFFu << (8 * i))) | ((uint32_t)q[i] << (8 * i));
     }
   }
+  return w;
+}
+
+// The same for k blocks 16 g .. 16 g + 15, in one load where the row allows it.
+__device__ __forceinline__ uint4 scale_words(const uint8_t* s, int64_t ld, int shift, int row, int rows, int g, int blocks) {
+  if (row < rows && 16 * g + 16 <= blocks) {
+    const uint8_t* q = s + (int64_t)(row >> shift) * ld + 16 * g;
+    if ((reinterpret_cast<uintptr_t>(q) & 15) == 0) return *reinterpret_cast<const uint4*>(q);
+  }
+  uint4 w;
+  w.x = scale_word(s, ld, shift, row, rows, 4 * g, blocks);
+  w.y = scale_word(s, ld, shift, row, rows, 4 * g + 1, blocks);
+  w.z = scale_word(s, ld, shift, row, rows, 4 * g + 2, blocks);
+  w.w = scale_word(s, ld, shift, row, rows, 4 * g + 3, blocks);
   return w;
 }
 
@@ -695,16 +709,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         int r0, c0, batch;
         bool mirror;
         place(tile, &r0, &c0, &batch, &mirror);
+        uint4 w[kWords];
         for (int g = 0; 4 * g < blocks; ++g, ++n) {
           const int ss = n % S::kScaleStages;
-          uint32_t w[kWords];
+          if ((g & 3) == 0) {
+            // 16 bytes of a row at once: single words of 350 rows kept the load path of the SM busy enough to slow
+            // the copies (8-bit 8192 x 8192 x 2048: 124 us; 114 with no loads of scales at all)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            w[i] = scale_word(p.sr, p.ld_sr, p.shift_r, r0 + t + 64 * i, p.rows, g, blocks);
+            for (int i = 0; i < 2; ++i)
+              w[i] = scale_words(p.sr, p.ld_sr, p.shift_r, r0 + t + 64 * i, p.rows, g / 4, blocks);
 #pragma unroll
-          for (int i = 2; i < kWords; ++i) {
-            const int c = t + 64 * (i - 2);
-            w[i] = scale_word(p.sc, p.ld_sc, p.shift_c, c < BN ? c0 + c : p.cols, p.cols, g, blocks);
+            for (int i = 2; i < kWords; ++i) {
+              const int c = t + 64 * (i - 2);
+              w[i] = scale_words(p.sc, p.ld_sc, p.shift_c, c < BN ? c0 + c : p.cols, p.cols, g / 4, blocks);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = make_uint4(w[i].y, w[i].z, w[i].w, 0);
           }
           // The slot is free once the stages of the group before last have been used up, which their own
           // barriers tell (a commit for the slot alone would cost the tensor cores another pause).  Stage
@@ -719,7 +740,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
             const int x = t + 64 * (i & 1);
-            *reinterpret_cast<uint32_t*>(dst + 512 * (i >> 1) + (x & 31) * 16 + (x >> 5) * 4) = w[i];
+            *reinterpret_cast<uint32_t*>(dst + 512 * (i >> 1) + (x & 31) * 16 + (x >> 5) * 4) = w[i].x;
           }
           tc::fence_async_shared();
           __syncwarp();

@@ -289,10 +289,9 @@ def _call(device: torch.device, stream, fn, *args):
 
 
 def _codes_room(rows: int, cols: int, block_rows: int, dtype, device):
-    """Codes [rows, cols] in rows of a multiple of 16 bytes, scales in rows of a
-    multiple of 4; and pointer and row stride of each for the call."""
+    """Codes [rows, cols] and scales in rows of a multiple of 16 bytes; and pointer and row stride of each for the call."""
     ld, blocks = -(-cols // 16) * 16, -(-cols // _BLOCK)
-    ld_s = -(-blocks // 4) * 4
+    ld_s = -(-blocks // 16) * 16
     q = torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device)
     s = torch.empty_strided((-(-rows // block_rows), blocks), (ld_s, 1), dtype=torch.float8_e8m0fnu, device=device)
     return (q, s), (q.data_ptr(), ld, s.data_ptr(), ld_s)
