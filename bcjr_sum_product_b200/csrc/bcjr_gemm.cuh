@@ -246,7 +246,7 @@ __device__ __forceinline__ void stage_products(uint32_t acc, uint32_t a, uint32_
 
 // ------------------------------------------------------------ small products
 
-constexpr int kTileThreads = 320;
+constexpr int kTileThreads = 576;
 
 template <int KIND, int BN>
 struct TileShape {
@@ -264,7 +264,7 @@ struct TileShape {
 
 // One block computes one 128 x BN tile over its share of k.  Warp 0 fills the
 // stages, one thread of warp 1 issues the products, warps 2 to 5 bring the
-// scales (MX), and warps 2 to 9 read the sums and store them, eight columns at a
+// scales (MX), and warps 2 to 17 read the sums and store them, eight columns at a
 // time in a loop that is not unrolled: each block runs it once, and fetching
 // straight-line code for 64 columns took longer than the stores (about 3 us).  Where there
 // are too few tiles for the GPU's SMs, a cluster of blocks splits k: each sends its
@@ -332,9 +332,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     *fail = 1;
     atomicCAS(&g_dense_error, 0, kErrTimeout);
   };
-  // the columns whose sums this warp finishes: units of eight, one in 2 * splits
+  // the columns whose sums this warp finishes: units of eight, one in 4 * splits
   const int row = r0 + 32 * (warp & 3) + lane;
-  const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 2 * p.splits;
+  const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 4 * p.splits;
   Ahead<8, PL> ahead;
 
   if (warp == 0) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     if (tc::elect_one()) tc::commit<1>(done);
     __syncwarp();
   } else {
-    const int t = threadIdx.x - 64;   // 0..255
+    const int t = threadIdx.x - 64;   // 0..511
     bool ok = true;
     if (KIND == MX && t < 128) {
       const int g1 = kb1 > kb0 ? (kb1 - 1) / 4 + 1 : kb0 / 4;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     tc::cluster_sync();
     if (warp >= 2) {
 #pragma unroll 2
-      for (int u = (warp - 2) >> 2; u < kUnits; u += 2) {
+      for (int u = (warp - 2) >> 2; u < kUnits; u += 4) {
         uint32_t w[8];
         if (some) {
           tc::tmem_ld8(sums + 8 * u, w);
