@@ -441,9 +441,17 @@ int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int gri
     const int most = values * (T == Q::IN_F32 ? 8 : 6);
     if (int rc = allow_smem(reinterpret_cast<const void*>(kern), &done[2 * e5m2 + row_blocks], most)) return rc;
   }
-  kern<<<grid, Q::kThreads, smem, st>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(Q::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
   counted_launch();
-  return cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA;
+  return BCJR_OK;
 }
 
 // From four rounds of tiles on, blocks stay (as many as fit the SMs: two, or one where

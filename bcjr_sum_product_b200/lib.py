@@ -244,7 +244,9 @@ _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4
 _WIDE = (torch.float32, torch.float16, torch.bfloat16)
 _CODES = (torch.float8_e4m3fn, torch.float8_e5m2)
 _SCALES = (torch.float8_e8m0fnu,)
+_SCALE_NAMES = {"a": "scale_a", "b": "scale_b"}
 _BLOCK = 128
+_empty = torch.empty_strided
 #: Coefficients of Muon's Newton-Schulz step (the default of orthogonalise and muon_step).
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
@@ -255,13 +257,15 @@ def _matrix(t: torch.Tensor, name: str, dtypes, ndim: int = 2, device=None) -> t
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != ndim:
+    stride = t.stride()
+    if len(stride) != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    if stride[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    if stride[-2] < shape[-1] and shape[-2] > 1:
-        raise ValueError(f"the rows of {name} must not overlap")
+    if not t.is_contiguous():
+        shape = t.shape
+        if stride[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        if stride[-2] < shape[-1] and shape[-2] > 1:
+            raise ValueError(f"the rows of {name} must not overlap")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
     return t
@@ -272,11 +276,16 @@ def _ld(t: torch.Tensor, multiple: int = 1) -> int:
     return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // multiple) * multiple
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of a device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _call(device: torch.device, stream, fn, *args):
     """fn(*args, stream handle) with the tensors' device current, on the given
     stream or that device's current one (allocations belong to it too)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        return fn(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
             return fn(*args, torch.cuda.current_stream().cuda_stream)
@@ -290,10 +299,10 @@ def _call(device: torch.device, stream, fn, *args):
 
 def _codes_room(rows: int, cols: int, block_rows: int, dtype, device):
     """Codes [rows, cols] and scales in rows of a multiple of 16 bytes; and pointer and row stride of each for the call."""
-    ld, blocks = -(-cols // 16) * 16, -(-cols // _BLOCK)
-    ld_s = -(-blocks // 16) * 16
-    q = torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device)
-    s = torch.empty_strided((-(-rows // block_rows), blocks), (ld_s, 1), dtype=torch.float8_e8m0fnu, device=device)
+    ld, blocks = (cols + 15) // 16 * 16, (cols + 127) // 128
+    ld_s = (blocks + 15) // 16 * 16
+    q = _empty((rows, cols), (ld, 1), dtype=dtype, device=device)
+    s = _empty((rows if block_rows == 1 else (rows + 127) // 128, blocks), (ld_s, 1), dtype=torch.float8_e8m0fnu, device=device)
     return (q, s), (q.data_ptr(), ld, s.data_ptr(), ld_s)
 
 
@@ -327,12 +336,14 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
 
 def _fp8_quantise(x, block_rows, dtype, minus, layout, st):
     rows, cols = x.shape
-    out, room = _codes_room(rows, cols, block_rows, dtype, x.device) if layout != "cols" else _NO_CODES
-    out_t, room_t = _codes_room(cols, rows, block_rows, dtype, x.device) if layout != "rows" else _NO_CODES
-    rc = load().bcjr_fp8_quantise(
-        x.data_ptr(), _TYPES[x.dtype], rows, cols, _ld(x), None if minus is None else minus.data_ptr(),
-        0 if minus is None else _ld(minus), _TYPES[dtype], block_rows, *room, *room_t, st)
-    _check(rc, "bcjr_fp8_quantise")
+    device = x.device
+    out, room = _codes_room(rows, cols, block_rows, dtype, device) if layout != "cols" else _NO_CODES
+    out_t, room_t = _codes_room(cols, rows, block_rows, dtype, device) if layout != "rows" else _NO_CODES
+    minus_p, ld_minus = (None, 0) if minus is None else (minus.data_ptr(), _ld(minus))
+    rc = load().bcjr_fp8_quantise(x.data_ptr(), _TYPES[x.dtype], rows, cols, _ld(x), minus_p, ld_minus, _TYPES[dtype],
+                                  block_rows, *room, *room_t, st)
+    if rc:
+        _check(rc, "bcjr_fp8_quantise")
     return out + out_t
 
 
@@ -341,7 +352,7 @@ def _scaled(q: torch.Tensor, scale: torch.Tensor, name: str, device):
     pointer, type and row stride of the codes, pointer and row stride of the
     scales, and the rows that share a scale."""
     _matrix(q, name, _CODES, device=device)
-    _matrix(scale, "scale_" + name, _SCALES, device=device)
+    _matrix(scale, _SCALE_NAMES[name], _SCALES, device=device)
     rows, cols = shape = q.shape
     have = scale.shape
     blocks = (cols + _BLOCK - 1) // _BLOCK
@@ -378,7 +389,7 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
 
 def _fp8_matmul(args_a, args_b, M, N, K, alpha, out_dtype, out, device, st):
     if out is None:
-        out, ld = torch.empty_strided((M, N), (N, 1), dtype=out_dtype, device=device), N
+        out, ld = _empty((M, N), (N, 1), dtype=out_dtype, device=device), N
     else:
         out_dtype, ld = out.dtype, _ld(out)
     rc = load().bcjr_fp8_matmul(*args_a, *args_b, M, N, K, alpha, out.data_ptr(), _TYPES[out_dtype], ld, st)
