@@ -245,8 +245,8 @@ constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 // The iterates and polynomials are kept in fp16 with headroom for entries up to
 // 16; the singular values of u / |u| lie in [0, 1].  False if, sampled over the
 // interval that each step can reach, the coefficients drive a singular value
-// above 2 or a + b t + c t^2 above 8.
-bool coeffs_bounded(const float* co, int steps) {
+// above 2 or |a + b t + c t^2| above 8.  `reach`: the largest of the latter for each step.
+bool coeffs_bounded(const float* co, int steps, float* reach) {
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
     const double a = co[3 * s], b = co[3 * s + 1], c = co[3 * s + 2];
@@ -257,6 +257,7 @@ bool coeffs_bounded(const float* co, int steps) {
       inner = std::max(inner, std::fabs(a + t * (b + t * c)));
     }
     if (!(most <= 2.0) || !(inner <= 8.0)) return false;
+    if (reach != nullptr) reach[s] = (float)inner;
     top = most;
   }
   return true;
@@ -270,31 +271,32 @@ int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps)
   if (sh.batch < 0 || sh.rows < 0 || sh.cols < 0) return BCJR_ERR_INVALID_ARG;
   if (steps < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return BCJR_ERR_INVALID_ARG;
   if (steps > kMaxSteps || sh.rows > kMaxMatrix || sh.cols > kMaxMatrix || sh.batch > kMaxBatch) return BCJR_ERR_UNSUPPORTED;
-  if (coeffs != nullptr && !coeffs_bounded(coeffs, steps)) return BCJR_ERR_INVALID_ARG;
+  if (coeffs != nullptr && !coeffs_bounded(coeffs, steps, nullptr)) return BCJR_ERR_INVALID_ARG;
   return BCJR_OK;
 }
 
-// P = X X^T (or X^T X), B = a I + b P + c P^2: x against itself, tiles up to the diagonal.
+// Symmetric products x y^T: P = X X^T (or X^T X), B = a I + b P + c P^2, and products of such matrices with one
+// another (polynomials of one matrix commute), tiles up to the diagonal.
 template <int BN, int EPI, bool MN, int PL>
-int sym_tile(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
+int sym_tile(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile);
   p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
   p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL > 1 ? 3 : 1), nsm);
-  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, x, p, true, st);
+  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, y, p, true, st);
 }
 template <int BN, int EPI, bool MN, int PL>
-int sym_pair(const Operand& x, G::Params p, int nsm, cudaStream_t st) {
+int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, 2 * G::kRowsTile);
   p.tiles_r = (int)t;
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
-  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, x, p, nsm, true, st);
+  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, y, p, nsm, true, st);
 }
 template <int EPI, bool MN, int PL>
-int run_sym(const Operand& x, const G::Params& p, int nsm, cudaStream_t st) {
+int run_sym(const Operand& x, const Operand& y, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, p, nsm, st);
-  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN, PL>(x, p, nsm, st);
-  return sym_tile<128, EPI, MN, PL>(x, p, nsm, st);
+  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, y, p, nsm, st);
+  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN, PL>(x, y, p, nsm, st);
+  return sym_tile<128, EPI, MN, PL>(x, y, p, nsm, st);
 }
 
 // X' = B X (or X B).
@@ -319,6 +321,17 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
   return iter_tile<128, EPI, R_MN, PL>(r, c, p, nsm, st);
 }
 
+// Whether two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
+// one Gram matrix of X and one product with X instead of two, for three more products of the shorter side's size.
+// Estimated from measured times: 5 us for each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s for Gram
+// matrices (whole flops), products with X and small symmetric products.  Not for three or more steps at once: the
+// error of P grows with every step that does not take it from X itself (two steps: as one at a time, 1e-3).
+bool worth_pairing(const Shape2& sh) {
+  const double m = (double)std::min(sh.rows, sh.cols), n = (double)std::max(sh.rows, sh.cols), b = (double)sh.batch;
+  const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 2 / 1.6e15);
+  return saved > 1.1 * 3.0 * (5.0 + 1e6 * b * m * m * m / 0.9e15);
+}
+
 template <int T>
 void launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
   Q::norm_kernel<T><<<dim3((unsigned)u.parts, (unsigned)batch), Q::kUpdateThreads, 0, st>>>(u);
@@ -340,14 +353,19 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   // warps take 512 columns of a row at a time; enough blocks of eight warps for every SM four times over
   const int64_t items = sh.rows * parts(sh.cols, Q::kSpan);
   u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
-  __half *x0, *x1, *pp, *bb;
+  __half *x0, *x1, *pp, *bb, *tt;
   double* partial;
+  const bool pairing = steps > 1 && worth_pairing(sh);
+  float flat[3 * kMaxSteps], reach[kMaxSteps];
+  for (int i = 0; i < 3 * steps; ++i) flat[i] = coeffs != nullptr ? coeffs[i] : kMuonCoeffs[i % 3];
+  coeffs_bounded(flat, steps, reach);
   auto layout = [&](Arena& ar) {
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
     x0 = ar.take<__half>((size_t)(sh.batch * PL * nx));
     x1 = ar.take<__half>((size_t)(sh.batch * PL * nx));
     pp = ar.take<__half>((size_t)(sh.batch * PL * np));
     bb = ar.take<__half>((size_t)(sh.batch * PL * np));
+    tt = pairing ? ar.take<__half>((size_t)(sh.batch * PL * np)) : nullptr;
   };
   Arena sizing;
   layout(sizing);
@@ -374,35 +392,47 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   else launch_update<Q::IN_BF16>(u, sh.batch, st);
   int rc = cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA;
 
-  for (int s = 0; s < steps && rc == BCJR_OK; ++s) {
-    const float* co = coeffs != nullptr ? coeffs + 3 * s : kMuonCoeffs;
+  G::Params p{};
+  p.rows = p.cols = (int)m;
+  p.batch = (int)sh.batch;
+  p.ld_out = p.ld_x = ld_p;
+  p.batch_out = p.batch_x = PL * np;
+  p.plane_out = p.plane_x = np;
+  const auto square = [&](const __half* at) { return Operand{at, m, m, ld_p, sh.batch * PL, np}; };
+  // out = B(x) with the coefficients of step s; out = x y
+  const auto polynomial = [&](__half* out, const __half* x, int s) {
+    p.k = (int)m;
+    p.out = out;
+    p.x = x;
+    p.fa = flat[3 * s];
+    p.fb = flat[3 * s + 1];
+    p.fc = flat[3 * s + 2];
+    return run_sym<G::POLY, false, PL>(square(x), square(x), p, nsm, st);
+  };
+  const auto product = [&](__half* out, const __half* x, const __half* y) {
+    p.k = (int)m;
+    p.out = out;
+    return run_sym<G::GRAM, false, PL>(square(x), square(y), p, nsm, st);
+  };
+  for (int s = 0; s < steps && rc == BCJR_OK;) {
+    // pairs of steps from the front, one alone before the last three if their number is odd; their product has to
+    // stay within fp16's headroom
+    const int left = steps - s;
+    const bool two = pairing && (left >= 4 || left == 2) && reach[s] * reach[s + 1] <= 15.f;
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
     const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * PL, nx};
-    G::Params p{};
-    p.rows = p.cols = (int)m;
     p.k = (int)(tall ? sh.rows : sh.cols);
-    p.batch = (int)sh.batch;
     p.out = pp;
-    p.ld_out = ld_p;
-    p.batch_out = PL * np;
-    p.plane_out = np;
-    rc = tall ? run_sym<G::GRAM, true, PL>(x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, p, nsm, st);
-    if (rc) break;
-    const Operand gram{pp, m, m, ld_p, sh.batch * PL, np};
-    p.k = (int)m;
-    p.out = bb;
-    p.x = pp;
-    p.ld_x = ld_p;
-    p.batch_x = PL * np;
-    p.plane_x = np;
-    p.fa = co[0];
-    p.fb = co[1];
-    p.fc = co[2];
-    if ((rc = run_sym<G::POLY, false, PL>(gram, p, nsm, st))) break;
+    rc = tall ? run_sym<G::GRAM, true, PL>(x, x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, x, p, nsm, st);
+    if (rc || (rc = polynomial(bb, pp, s))) break;
+    if (two && ((rc = product(tt, bb, pp)) || (rc = product(pp, tt, bb)) || (rc = polynomial(tt, pp, s + 1)) ||
+                (rc = product(pp, tt, bb))))
+      break;
+    s += two ? 2 : 1;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
-    const Operand poly{bb, m, m, ld_p, sh.batch * PL, np};
-    const bool end = s + 1 == steps;
+    const Operand poly = square(two ? pp : bb);
+    const bool end = s == steps;
     G::Params q = end ? last : G::Params{};
     q.rows = (int)sh.cols;
     q.cols = (int)sh.rows;

@@ -40,7 +40,7 @@ constexpr int kErrTimeout = 4;
 enum Kind { F16 = 0, MX = 1 };
 enum Epilogue {
   OUT = 0,    // out = alpha D
-  GRAM = 1,   // P = D, symmetric, both halves stored
+  GRAM = 1,   // P = D, symmetric, both halves stored (also a product of two polynomials of one P)
   POLY = 2,   // B = a I + b P + c D, symmetric, both halves stored
   ITER = 3,   // X' = D
   LAST = 4,   // out = D
