@@ -50,8 +50,8 @@ MUON = (3.4445, -4.7750, 2.0315)
 
 
 def newton_schulz(g, steps=5, coeffs=None, eps=1e-7):
-    """The iteration on the last two dimensions, fp64."""
-    x = torch.as_tensor(g).detach().cpu().double()
+    """The iteration on the last two dimensions, fp64 (on g's device)."""
+    x = torch.as_tensor(g).detach().double()
     x = x / (torch.linalg.vector_norm(x, dim=(-2, -1), keepdim=True) + eps)
     for s in range(steps):
         a, b, c = coeffs[s] if coeffs is not None else MUON

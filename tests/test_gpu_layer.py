@@ -241,7 +241,7 @@ def check_orthogonal(out, g, steps=5, coeffs=None, noise=15.0):
     and they may grow twice as fast as the matrix itself where its singular values
     lie within a factor of a few of one another (the polynomial's slope there against
     its mean slope); then one rounding to the output's type."""
-    want = ref.newton_schulz(g, steps, coeffs)
+    want = ref.newton_schulz(g, steps, coeffs).cpu()
     tol = 2 * noise * 2.0 ** -11 + HALF_STEP[out.dtype]
     err = out.cpu().double() - want
     rel = torch.linalg.vector_norm(err, dim=(-2, -1)) / torch.linalg.vector_norm(want, dim=(-2, -1))
@@ -264,6 +264,21 @@ def test_orthogonalise_large(rows, cols):
     out = lib.orthogonalise(g.to(DEV))
     finished()
     check_orthogonal(out, g)
+
+
+@pytest.mark.parametrize("rows,cols", [(1536, 6145), (6200, 1500)])
+@pytest.mark.parametrize("steps,coeffs", [(1, None), (2, None), (3, None), (4, None), (5, None), (2, (1.875, -1.25, 0.375)),
+                                          (2, [(6.5, -17.0, 12.0), (2.5, -2.2, 0.6)])])
+def test_orthogonalise_long_matrices(rows, cols, steps, coeffs):
+    """Long enough that steps are taken two at a time (but for the last case, whose
+    polynomials' product would leave fp16's headroom).  A pair rounds X once and P, B, P
+    again, B and two products between them: five relative errors of 2^-11 more than the
+    six of two single steps."""
+    g = randn(rows, cols, seed=25).to(DEV)
+    co = None if coeffs is None else [coeffs] * steps if isinstance(coeffs, tuple) else coeffs
+    out = lib.orthogonalise(g, steps=steps, coeffs=coeffs)
+    finished()
+    check_orthogonal(out, g, steps, co, noise=3.0 * steps + 5.0 * (steps // 2))
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 40), (30, 30), (130, 333), (333, 130), (512, 700), (1300, 1400), (1500, 1300)])
