@@ -57,12 +57,17 @@ int scratch_alloc(void** mem, size_t bytes, cudaStream_t st) {
       props.location.type = cudaMemLocationTypeDevice;
       props.location.id = dev;
       cudaMemPool_t p;
-      if (cudaMemPoolCreate(&p, &props) != cudaSuccess) {
+      // the first call may come while a graph is captured, which a pool's creation is no part of
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      cudaThreadExchangeStreamCaptureMode(&mode);
+      const cudaError_t made = cudaMemPoolCreate(&p, &props);
+      uint64_t thr = UINT64_MAX;
+      if (made == cudaSuccess) cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &thr);
+      cudaThreadExchangeStreamCaptureMode(&mode);
+      if (made != cudaSuccess) {
         cudaGetLastError();
         return BCJR_ERR_CUDA;
       }
-      uint64_t thr = UINT64_MAX;
-      cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &thr);
       g_pool[dev] = p;
     }
     pool = g_pool[dev];

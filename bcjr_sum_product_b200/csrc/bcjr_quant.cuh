@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "bcjr_tc.cuh"
+
 namespace bcjr {
 namespace quant {
 
@@ -339,6 +341,7 @@ template <int T>
 __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams p) {
   using X = typename In<T>::type;
   __shared__ double part[8];
+  tc::launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int spans = (p.cols + kSpan - 1) / kSpan;
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
@@ -366,11 +369,9 @@ __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams
         }
       }
     }
-    // squares in fp32, their sums in fp64 (16 at a time: nothing is lost to a long sum)
-    float s = 0.f;
+    // in fp64: squares of fp32 values neither overflow nor vanish, and nothing is lost to a long sum
 #pragma unroll
-    for (int j = 0; j < 16; ++j) s = fmaf(u[j], u[j], s);
-    sum += (double)s;
+    for (int j = 0; j < 16; ++j) sum = fma((double)u[j], (double)u[j], sum);
   }
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane == 0) part[warp] = sum;
@@ -381,12 +382,15 @@ __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams
   }
 }
 
-// Second pass: X_0 = u / (|u| + eps), scaled, as fp16.
+// Second pass: X_0 = u / (|u| + eps), scaled, as fp16.  From the last row to the first: what
+// the first pass touched last is still in L2.
 template <int T>
 __global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParams p) {
   using X = typename In<T>::type;
   __shared__ double part[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tc::launch_dependents();
+  tc::wait_for_earlier();
   // every block adds up all parts in the same order
   double sum = 0.0;
   for (int i = threadIdx.x; i < p.parts; i += kUpdateThreads) sum += p.partial[(int64_t)blockIdx.y * p.parts + i];
@@ -395,12 +399,16 @@ __global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParam
   __syncthreads();
   sum = 0.0;
   for (int w = 0; w < 8; ++w) sum += part[w];
-  const float f = (float)((double)p.scale / (sqrt(sum) + (double)p.eps));
+  // the factor as a power of two and the rest, since it may lie outside fp32's range (a multiplication by a power of
+  // two rounds nothing unless the result underflows)
+  const double factor = (double)p.scale / (sqrt(sum) + (double)p.eps);
+  const int e = factor > 0.0 && factor < 1e300 ? ilogb(factor) / 2 : 0;
+  const float f2 = (float)ldexp(1.0, e), f = (float)ldexp(factor, -e);
   const int spans = (p.cols + kSpan - 1) / kSpan;
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
   __half* x = p.x + blockIdx.y * p.batch_x;
   for (int i = blockIdx.x * 8 + warp; i < p.rows * spans; i += gridDim.x * 8) {
-    const int r = i / spans, c = (i - r * spans) * kSpan + 4 * lane;
+    const int at_row = i / spans, r = p.rows - 1 - at_row, c = (i - at_row * spans) * kSpan + 4 * lane;
     float u[16], m[16];
     const float* mp = p.momentum == nullptr ? nullptr : p.momentum + (int64_t)r * p.ld_m;
     load_span<T>(p, g + (int64_t)r * p.ld_g, mp, c, u, m);
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParam
       alignas(8) __half h[4], l[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float v = (mp == nullptr ? u[4 * j + k] : update_of(p, u[4 * j + k], m[4 * j + k])) * f;
+        const float v = (mp == nullptr ? u[4 * j + k] : update_of(p, u[4 * j + k], m[4 * j + k])) * f2 * f;
         h[k] = __float2half_rn(v);
         l[k] = __float2half_rn(v - __half2float(h[k]));
       }

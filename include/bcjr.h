@@ -276,7 +276,11 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  *   out     [batch][rows][cols]  fp16 or bf16 (output)
  * batch <= 32767, rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.  Coefficients that drive a
  * singular value of [0, 1] above 2 are BCJR_ERR_INVALID_ARG.  A matrix of zeros
- * gives zeros (eps > 0); NaN or infinities make that matrix NaN.
+ * gives zeros (eps > 0); NaN or infinities make that matrix NaN.  Entries of X_0
+ * below 2^-36 vanish (so does a G whose norm is that far below eps).  Directions
+ * whose singular values are small against ||G||_F are amplified (Muon's default: up
+ * to 485 times), rounding with them: where only those carry the result, as with a
+ * matrix of few strong directions, the error of a bf16 out grows to some percent.
  */
 BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g,
                                 int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out,

@@ -318,6 +318,20 @@ def test_orthogonalise_not_finite_matrix_stays_alone():
     assert torch.isnan(out[1]).all()
 
 
+@pytest.mark.parametrize("exponent", [-130, -60, 60, 110])
+def test_orthogonalise_does_not_depend_on_scale(exponent):
+    """A power of two on the matrix moves neither the norm's rounding nor any other while
+    its entries stay normal numbers; with eps = 0 the result is the same bits."""
+    g = randn(70, 200, seed=26).to(torch.bfloat16).float()
+    if exponent == -130:
+        g = torch.where(g.abs() < 2.0 ** -4, torch.zeros(()), g.sign() * torch.exp2(g.abs().log2().floor()))   # powers of two: exact below 2^-126 too
+    one = lib.orthogonalise(g.to(DEV), eps=0.0)
+    out = lib.orthogonalise((g.double() * 2.0 ** exponent).float().to(DEV), eps=0.0)
+    finished()
+    assert torch.equal(out, one)
+    check_orthogonal(one, g)
+
+
 def test_orthogonalise_coefficients_of_each_step():
     g = randn(50, 140, seed=24)
     coeffs = [(3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)]

@@ -1,6 +1,9 @@
 """The layer-wise QAT operators together, as the driver runs them, and how they may
 be called: streams, graphs, views, in sequence and at once."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -255,6 +258,33 @@ def test_graphs():
         finished()
         for (_, _, _, _, out), wt in zip(graphs, want):
             assert same(bits(out), wt)
+
+
+def test_first_calls_inside_a_capture():
+    """Nothing that a first call sets up (attributes, entry points, the scratch pool)
+    disturbs a capture; in a process of its own, where they are the first."""
+    code = """
+import torch
+from bcjr_sum_product_b200 import lib
+x, w = torch.randn(300, 520, device="cuda"), torch.randn(300, 520, device="cuda")
+m = torch.zeros_like(x)
+big = torch.randn(2048, 2048, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q = lib.fp8_quantise(x, layout="both")
+    y = lib.fp8_matmul(*q[:2], *q[:2])
+    o = lib.orthogonalise(x)
+    p = lib.orthogonalise(big)
+    lib.muon_step(w, x, m, 0.1)
+g.replay()
+torch.cuda.synchronize()
+assert lib.get_device_error() == 0
+assert torch.equal(o, lib.orthogonalise(x)) and torch.equal(p, lib.orthogonalise(big)) and torch.equal(y, lib.fp8_matmul(*q[:2], *q[:2]))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 def test_offsets_past_32_bits():
