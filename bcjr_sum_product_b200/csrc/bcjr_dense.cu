@@ -369,7 +369,11 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   // warps take 512 columns of a row at a time; enough blocks of eight warps for every SM four times over
   const int64_t items = sh.rows * parts(sh.cols, Q::kSpan);
   u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
-  __half *x0, *x1, *pp, *bb, *tt;
+  __half *x0, *x1;
+  struct Square {           // a symmetric matrix and what rounding took from its diagonal
+    __half* at;
+    float *diff, *quot;
+  } pp{}, bb{}, tt{};
   double* partial;
   const bool pairing = steps > 1 && worth_pairing(sh);
   float flat[3 * kMaxSteps], reach[kMaxSteps];
@@ -379,9 +383,12 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
     x0 = ar.take<__half>((size_t)(sh.batch * PL * nx));
     x1 = ar.take<__half>((size_t)(sh.batch * PL * nx));
-    pp = ar.take<__half>((size_t)(sh.batch * PL * np));
-    bb = ar.take<__half>((size_t)(sh.batch * PL * np));
-    tt = pairing ? ar.take<__half>((size_t)(sh.batch * PL * np)) : nullptr;
+    for (Square* q : {&pp, &bb, &tt}) {
+      if (q == &tt && !pairing) continue;
+      q->at = ar.take<__half>((size_t)(sh.batch * PL * np));
+      q->diff = ar.take<float>((size_t)(sh.batch * ld_p));
+      q->quot = ar.take<float>((size_t)(sh.batch * ld_p));
+    }
   };
   Arena sizing;
   layout(sizing);
@@ -412,20 +419,35 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   p.ld_out = p.ld_x = ld_p;
   p.batch_out = p.batch_x = PL * np;
   p.plane_out = p.plane_x = np;
-  const auto square = [&](const __half* at) { return Operand{at, m, m, ld_p, sh.batch * PL, np}; };
+  p.ld_dev = ld_p;
+  // What rounding takes from the diagonals is kept for sides of up to 256 (gemm::finish): a bf16 result's error is 1.1 to
+  // 1.2 times that of rounding the exact result with it, up to 1.7 without (160 x 6788); from 256 on 1.1 to 1.3 without,
+  // where it would cost 2 to 4 % (16 x 333 x 130: 84 us without, 94 with).
+  const bool diagonals = PL == 1 && m <= 256;
+  const auto square = [&](const Square& q) { return Operand{q.at, m, m, ld_p, sh.batch * PL, np}; };
+  const auto into = [&](const Square& out, int64_t k) {
+    p.k = (int)k;
+    p.out = out.at;
+    p.diff_out = diagonals ? out.diff : nullptr;
+    p.quot_out = diagonals ? out.quot : nullptr;
+    p.dev_r = p.dev_c = nullptr;
+  };
   // out = B(x) with the coefficients of step s; out = x y
-  const auto polynomial = [&](__half* out, const __half* x, int s) {
-    p.k = (int)m;
-    p.out = out;
-    p.x = x;
+  const auto polynomial = [&](const Square& out, const Square& x, int s) {
+    into(out, m);
+    p.x = x.at;
+    if (diagonals) p.dev_r = p.dev_c = x.diff;
     p.fa = flat[3 * s];
     p.fb = flat[3 * s + 1];
     p.fc = flat[3 * s + 2];
     return run_sym<G::POLY, false, PL>(square(x), square(x), p, nsm, st);
   };
-  const auto product = [&](__half* out, const __half* x, const __half* y) {
-    p.k = (int)m;
-    p.out = out;
+  const auto product = [&](const Square& out, const Square& x, const Square& y) {
+    into(out, m);
+    if (diagonals) {
+      p.dev_r = x.quot;
+      p.dev_c = y.quot;
+    }
     return run_sym<G::GRAM, false, PL>(square(x), square(y), p, nsm, st);
   };
   for (int s = 0; s < steps && rc == BCJR_OK;) {
@@ -436,8 +458,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
     const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * PL, nx};
-    p.k = (int)(tall ? sh.rows : sh.cols);
-    p.out = pp;
+    into(pp, tall ? sh.rows : sh.cols);
     rc = tall ? run_sym<G::GRAM, true, PL>(x, x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, x, p, nsm, st);
     if (rc || (rc = polynomial(bb, pp, s))) break;
     if (two && ((rc = product(tt, bb, pp)) || (rc = product(pp, tt, bb)) || (rc = polynomial(tt, pp, s + 1)) ||
@@ -445,13 +466,16 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
       break;
     s += two ? 2 : 1;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
-    const Operand poly = square(two ? pp : bb);
+    const Square& b = two ? pp : bb;
+    const Operand poly = square(b);
     const bool end = s == steps;
     G::Params q = end ? last : G::Params{};
     q.rows = (int)sh.cols;
     q.cols = (int)sh.rows;
     q.k = (int)m;
     q.batch = (int)sh.batch;
+    q.ld_dev = ld_p;
+    if (diagonals) (tall ? q.dev_r : q.dev_c) = b.quot;
     if (!end) {
       q.out = x1;
       q.ld_out = ld_x;
@@ -597,7 +621,7 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
   G::Params last{};
   last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one plane of 11 bits leaves less than bf16's own rounding; fp16 shows more
+  // one plane of 11 bits leaves an error of about 1e-3, less than bf16's own rounding (1.7e-3); fp16 shows more
   return out_type == BCJR_BF16 ? run_newton_schulz<1>(sh, u, g_type, steps, coeffs, G::LAST, last, st)
                                : run_newton_schulz<2>(sh, u, g_type, steps, coeffs, G::LAST, last, st);
 }

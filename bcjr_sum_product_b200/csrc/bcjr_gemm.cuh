@@ -72,6 +72,11 @@ struct Params {
   // epilogue
   void* out;
   const __half* x;           // P (POLY), laid out as D
+  // What rounding took from the diagonals of the symmetric matrices (one plane; see finish): of the operands along r
+  // and along c, or null, and of the result.  POLY: the differences; else the quotients.
+  const float *dev_r, *dev_c;
+  float *diff_out, *quot_out;   // or null
+  int64_t ld_dev;            // from one matrix of the batch to the next
   int64_t ld_out, ld_x;
   int64_t batch_out, batch_x;
   int64_t plane_out, plane_x;   // PL = 2: from one plane to the other
@@ -103,6 +108,7 @@ __device__ __forceinline__ void store_columns(void* out, int64_t at, int64_t ld,
 template <int W, int PL>
 struct Ahead {
   uint4 h[PL][W / 8];
+  float4 dev[W / 4];         // of the columns
 };
 template <int EPI, int W, int PL>
 __device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W, PL>& a) {
@@ -112,36 +118,81 @@ __device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r
     for (int l = 0; l < PL; ++l)
 #pragma unroll
       for (int i = 0; i < W / 8; ++i)
-        a.h[l][i] = c0 + 8 * i < p.cols ? *reinterpret_cast<const uint4*>(x + l * p.plane_x + 8 * i) : make_uint4(0, 0, 0, 0);
+        a.h[l][i] = c0 + 8 * i < p.cols ? __ldcg(reinterpret_cast<const uint4*>(x + l * p.plane_x + 8 * i)) : make_uint4(0, 0, 0, 0);
   }
+  if (PL == 1 && EPI != OUT && p.dev_c != nullptr) {
+    const float* d = p.dev_c + batch * p.ld_dev + c0;
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      a.dev[i] = c0 + 4 * i < p.cols ? __ldcg(reinterpret_cast<const float4*>(d + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+// The row's own deviation.
+template <int EPI, int PL>
+__device__ __forceinline__ float row_deviation(const Params& p, int64_t batch, int r) {
+  if (PL > 1 || EPI == OUT || p.dev_r == nullptr || r >= p.rows) return EPI == POLY ? 0.f : 1.f;
+  return __ldcg(p.dev_r + batch * p.ld_dev + r);
 }
 
 // Stores columns c0..c0+W-1 (as far as they exist) of row r.
+//
+// The diagonals of the symmetric matrices of a small or long X are nearly constant, so their roundings to 11 bits all
+// go the same way, and a few steps of that are an error of 2.4e-3 (160 x 6788) where independent roundings leave
+// 0.8e-3.  Where `diff_out` and the others are given, what rounding took from a diagonal is therefore kept in fp32: as a
+// difference d, with which P^2 is
+// (P16^2)_rc + P_rc (d_r + d_c) to first order, and as a quotient, by which the rows and columns of the other
+// products are multiplied (right for the diagonal's part of the sum, and nothing next to the rest's own rounding).
 template <int EPI, int W, int PL>
-__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead<W, PL>& a,
-                                       float (&v)[W]) {
+__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, float dev_row,
+                                       const Ahead<W, PL>& a, float (&v)[W]) {
   if (r >= p.rows) return;
   const int n = p.cols - c0;
   const int64_t at = batch * p.batch_out + (int64_t)c0 * p.ld_out + r;
   const float unit = EPI == OUT ? p.fa : EPI == LAST ? 1.f / (kIterScale * kIterScale) : 1.f / kIterScale;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] *= unit;
+  if constexpr (PL == 1 && EPI != OUT && EPI != POLY) {
+    if (p.dev_c != nullptr) {
+      const float* d = reinterpret_cast<const float*>(a.dev);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] *= dev_row * d[i];
+    } else if (p.dev_r != nullptr) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] *= dev_row;
+    }
+  }
   if constexpr (EPI == OUT || EPI == LAST) {
     if (p.out_type == OUT_F32) store_columns<OUT_F32, W>(p.out, at, p.ld_out, n, v);
     else if (p.out_type == OUT_F16) store_columns<OUT_F16, W>(p.out, at, p.ld_out, n, v);
     else store_columns<OUT_BF16, W>(p.out, at, p.ld_out, n, v);
   } else if constexpr (EPI == GRAM || EPI == POLY || EPI == ITER) {
+    const int warp_row = r & ~31;
+    const bool diagonal = c0 < warp_row + 32 && c0 + W > warp_row;   // it passes through the warp's rows
     if constexpr (EPI == POLY) {
       const __half* x = reinterpret_cast<const __half*>(a.h);   // W values, then what they left
+      const float* d = reinterpret_cast<const float*>(a.dev);
+      const float on_diagonal = fmaf(p.fa, kIterScale, PL == 1 ? p.fb * dev_row : 0.f);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const float pv = PL > 1 ? __half2float(x[i]) + __half2float(x[(PL - 1) * W + i]) : __half2float(x[i]);
+        if (PL == 1 && p.dev_c != nullptr) v[i] = fmaf(pv * (1.f / kIterScale), dev_row + d[i], v[i]);
         v[i] = fmaf(p.fb, pv, p.fc * v[i]);
-        if (c0 + i == r) v[i] += p.fa * kIterScale;
+      }
+      if (diagonal) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = fmaf(i == r - c0 ? 1.f : 0.f, on_diagonal, v[i]);
       }
     }
-    __half* const o = static_cast<__half*>(p.out) + at;
-    __half* const m = static_cast<__half*>(p.out) + batch * p.batch_out + (int64_t)r * p.ld_out + c0;   // 16-byte aligned
+    // (as a sum of products with 0 and 1: a selection becomes an index into local memory)
+    float exact = 0.f;
+    const bool keep = PL == 1 && EPI != ITER && diagonal && p.diff_out != nullptr;
+    if (keep) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        v[i] = i < n ? v[i] : 0.f;     // columns that do not exist hold anything, NaN too
+        exact = fmaf(i == r - c0 ? 1.f : 0.f, v[i], exact);
+      }
+    }
 #pragma unroll
     for (int plane = 0; plane < PL; ++plane) {
       alignas(16) __half h[W];
@@ -150,18 +201,24 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
         h[i] = __float2half_rn(v[i]);
         if (PL > 1) v[i] -= __half2float(h[i]);
       }
-      __half* to = o + plane * p.plane_out;
+      if (keep && (unsigned)(r - c0) < (unsigned)W) {
+        const float back = __half2float(__float2half_rn(exact));
+        p.diff_out[batch * p.ld_dev + r] = exact - back;
+        p.quot_out[batch * p.ld_dev + r] = back != 0.f ? __fdividef(exact, back) : 1.f;   // 1 to within 2^-11: full precision is not needed
+      }
+      __half* to = static_cast<__half*>(p.out) + at + plane * p.plane_out;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         if (i < n) *to = h[i];
         to += p.ld_out;
       }
       if (EPI != ITER && mirror) {
+        // the row's own values, side by side: 16-byte aligned; whole groups of 8 stay inside the row's room
+        // (ld_out is the columns rounded up to 8)
+        __half* m = static_cast<__half*>(p.out) + batch * p.batch_out + plane * p.plane_out + (int64_t)r * p.ld_out + c0;
 #pragma unroll
-        for (int j = 0; j < W / 8; ++j) {
-          // whole groups of 8 stay inside the row's room (ld_out is the columns rounded up to 8)
-          if (8 * j < n) reinterpret_cast<uint4*>(m + plane * p.plane_out)[j] = reinterpret_cast<const uint4*>(h)[j];
-        }
+        for (int j = 0; j < W / 8; ++j)
+          if (8 * j < n) reinterpret_cast<uint4*>(m)[j] = reinterpret_cast<const uint4*>(h)[j];
       }
     }
   } else {   // STEP
@@ -336,6 +393,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   const int row = r0 + 32 * (warp & 3) + lane;
   const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 4 * p.splits;
   Ahead<8, PL> ahead;
+  float dev_row = 1.f;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -425,6 +483,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
       }
     }
     if (unit0 < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c0 + 8 * unit0, ahead);
+    dev_row = row_deviation<EPI, PL>(p, batch, row);
     ok = ok && tc::mbar_wait(done, 0);
     if (!ok) gave_up();
   }
@@ -485,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
       }
       const Ahead<8, PL> now = ahead;
       if (u + step < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c + 8 * step, ahead);
-      finish<EPI, 8, PL>(p, batch, row, c, mirror, now, v);
+      finish<EPI, 8, PL>(p, batch, row, c, mirror, dev_row, now, v);
     }
   }
   tc::fence_before();
@@ -764,6 +823,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       Ahead<16, PL> ahead;
       uint32_t u[16];
       load_ahead<EPI, 16, PL>(p, batch, row, c0 + 16 * first, ahead);
+      const float dev_row = row_deviation<EPI, PL>(p, batch, row);
       ok = tc::mbar_wait(accfull + 8 * set, (n / S::kSets) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
       if (!ok) break;
@@ -781,7 +841,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
           tc::tmem_ld16(sums + set * BN + c + 32, u);
           load_ahead<EPI, 16, PL>(p, batch, row, c0 + c + 32, ahead);
         }
-        finish<EPI, 16, PL>(p, batch, row, c0 + c, mirror, now, v);
+        finish<EPI, 16, PL>(p, batch, row, c0 + c, mirror, dev_row, now, v);
       }
       tc::tmem_drain_ld();
       tc::fence_before();

@@ -324,14 +324,17 @@ __device__ __forceinline__ void load_span(const UpdateParams& p, const typename 
     for (int j = 0; j < 4; ++j) In<T>::get4(g + c + 128 * j, *reinterpret_cast<float(*)[4]>(&u[4 * j]));
     if (m != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) In<IN_F32>::get4(m + c + 128 * j, *reinterpret_cast<float(*)[4]>(&mv[4 * j]));
+      for (int j = 0; j < 4; ++j) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(m + c + 128 * j));
+        mv[4 * j] = q.x; mv[4 * j + 1] = q.y; mv[4 * j + 2] = q.z; mv[4 * j + 3] = q.w;
+      }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int at = c + 128 * (j / 4) + j % 4;
       u[j] = at < p.cols ? In<T>::get(g[at]) : 0.f;
-      mv[j] = m != nullptr && at < p.cols ? m[at] : 0.f;
+      mv[j] = m != nullptr && at < p.cols ? __ldcg(m + at) : 0.f;
     }
   }
 }
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kUpdateThreads) start_kernel(const UpdateParam
   tc::wait_for_earlier();
   // every block adds up all parts in the same order
   double sum = 0.0;
-  for (int i = threadIdx.x; i < p.parts; i += kUpdateThreads) sum += p.partial[(int64_t)blockIdx.y * p.parts + i];
+  for (int i = threadIdx.x; i < p.parts; i += kUpdateThreads) sum += __ldcg(p.partial + (int64_t)blockIdx.y * p.parts + i);
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane == 0) part[warp] = sum;
   __syncthreads();

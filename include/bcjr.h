@@ -267,7 +267,7 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * when rows > cols), out is the last X: G with its singular values moved
  * towards 1.  Products sum in fp32.  For a bf16 out their operands, the iterates
  * and Gram matrices, are fp16 scaled by 2^12 (11 bits), which keeps out within
- * about 1.5e-3 of the exact iteration in the 2-norm, less than its own rounding;
+ * about 1e-3 of the exact iteration in the 2-norm, less than its own rounding;
  * for an fp16 out they are pairs of such values (22 bits, three times the
  * products), and out is within about 2e-5 before it is rounded.
  *   g       [batch][rows][cols]  fp32, fp16 or bf16 (input)

@@ -299,6 +299,21 @@ def test_orthogonalise_two_planes(rows, cols):
     assert rel <= 2.5e-4
 
 
+@pytest.mark.parametrize("rows,cols", [(16, 100), (16, 16), (40, 40), (3652, 16), (64, 300), (33, 5000), (160, 6788), (5632, 165)])
+def test_orthogonalise_roundings_do_not_add_up(rows, cols):
+    """Of thin and long matrices the diagonals of P and B are nearly constant, so that plain
+    roundings to 11 bits (2^-12 on average, fifteen of them) would all go one way: up to
+    15 * 2^-12 = 3.7e-3.  Independent ones add up to sqrt(15) * 2^-12 / sqrt(3) * 2 =
+    1.1e-3 (twice for the growth of small singular values), and with the result's own
+    rounding, at most 2^-8 / sqrt(3) = 2.3e-3 in the 2-norm, to 2.5e-3."""
+    g = randn(rows, cols, seed=27) + randn(rows, 4, seed=28) @ randn(4, cols, seed=29)
+    out = lib.orthogonalise(g.to(DEV))
+    finished()
+    want = ref.newton_schulz(g)
+    rel = float(torch.linalg.vector_norm(out.cpu().double() - want) / torch.linalg.vector_norm(want))
+    assert rel <= 2.5e-3
+
+
 def test_orthogonalise_batch_strides_and_zeros():
     g = randn(5, 60, 200, seed=22).to(DEV)
     g[2] = 0
@@ -330,6 +345,19 @@ def test_orthogonalise_does_not_depend_on_scale(exponent):
     finished()
     assert torch.equal(out, one)
     check_orthogonal(one, g)
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 200), (201, 70), (130, 333), (13, 13), (517, 600), (1537, 6145)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16])
+def test_orthogonalise_after_not_finite_values(rows, cols, out_dtype):
+    """What an earlier call left in the scratch memory (NaN here) does not matter."""
+    g = randn(rows, cols, seed=30).to(DEV)
+    want = lib.orthogonalise(g, out_dtype=out_dtype)
+    for bad in (math.nan, math.inf):
+        spoilt = lib.orthogonalise(torch.full_like(g, bad), out_dtype=out_dtype)
+        assert torch.isnan(spoilt).all()
+        assert torch.equal(lib.orthogonalise(g, out_dtype=out_dtype), want)
+    finished()
 
 
 def test_orthogonalise_coefficients_of_each_step():
