@@ -420,10 +420,11 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   p.batch_out = p.batch_x = PL * np;
   p.plane_out = p.plane_x = np;
   p.ld_dev = ld_p;
-  // What rounding takes from the diagonals is kept for sides of up to 256 (gemm::finish): a bf16 result's error is 1.1 to
-  // 1.2 times that of rounding the exact result with it, up to 1.7 without (160 x 6788); from 256 on 1.1 to 1.3 without,
-  // where it would cost 2 to 4 % (16 x 333 x 130: 84 us without, 94 with).
-  const bool diagonals = PL == 1 && m <= 256;
+  // What rounding takes from the diagonals is kept (gemm::finish) where they are nearly constant: for shorter sides of up
+  // to 64, and of up to 256 in long matrices.  A bf16 result's error is then 1.1 to 1.2 times that of rounding the exact
+  // result; without it up to 1.7 (160 x 6788), but at most 1.35 in the others, where it would cost up to 14 % (16 x 333 x
+  // 130: 92 us without, 106 with).
+  const bool diagonals = PL == 1 && (m <= 64 || (m <= 256 && std::max(sh.rows, sh.cols) >= 4 * m));
   const auto square = [&](const Square& q) { return Operand{q.at, m, m, ld_p, sh.batch * PL, np}; };
   const auto into = [&](const Square& out, int64_t k) {
     p.k = (int)k;
