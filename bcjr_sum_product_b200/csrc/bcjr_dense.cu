@@ -208,7 +208,7 @@ int matmul_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)tiles;
   p.splits = splits_for(tiles, parts(p.k, 128), nsm);
-  return launch_tile<G::MX, BN, false, false, G::OUT, 1>(r, c, p, false, st);
+  return launch_tile<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, false, st);
 }
 template <int BN>
 int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
@@ -216,7 +216,7 @@ int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   if (tiles > INT32_MAX / 2) return BCJR_ERR_UNSUPPORTED;
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)tiles;
-  return launch_pair<G::MX, BN, false, false, G::OUT, 1>(r, c, p, nsm, false, st);
+  return launch_pair<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, nsm, false, st);
 }
 
 int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
@@ -283,7 +283,7 @@ template <int BN, int EPI, bool MN, int PL>
 int sym_tile(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile);
   p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL > 1 ? 3 : 1), nsm);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
   return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, y, p, true, st);
 }
 template <int BN, int EPI, bool MN, int PL>
@@ -306,7 +306,7 @@ template <int BN, int EPI, bool R_MN, int PL>
 int iter_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL > 1 ? 3 : 1), nsm);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
   return launch_tile<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, true, st);
 }
 template <int BN, int EPI, bool R_MN, int PL>
@@ -355,7 +355,7 @@ int launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
   return BCJR_OK;
 }
 
-// The whole iteration, with iterates of PL planes; `last` holds the epilogue of the last product (out, its
+// The whole iteration, with iterates held as PL says; `last` holds the epilogue of the last product (out, its
 // layout and type, the weights' factors) and says which by `epi`.
 template <int PL>
 int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi,
@@ -381,11 +381,12 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   coeffs_bounded(flat, steps, reach);
   auto layout = [&](Arena& ar) {
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
-    x0 = ar.take<__half>((size_t)(sh.batch * PL * nx));
-    x1 = ar.take<__half>((size_t)(sh.batch * PL * nx));
+    x0 = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * nx));
+    x1 = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * nx));
     for (Square* q : {&pp, &bb, &tt}) {
       if (q == &tt && !pairing) continue;
-      q->at = ar.take<__half>((size_t)(sh.batch * PL * np));
+      q->at = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * np));
+      if (PL != G::ONE_EXACT) continue;
       q->diff = ar.take<float>((size_t)(sh.batch * ld_p));
       q->quot = ar.take<float>((size_t)(sh.batch * ld_p));
     }
@@ -401,9 +402,9 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   u.partial = partial;
   u.x = x0;
   u.ld_x = ld_x;
-  u.batch_x = PL * nx;
+  u.batch_x = G::planes(PL) * nx;
   u.plane_x = nx;
-  u.planes = PL;
+  u.planes = G::planes(PL);
   u.rows = (int)sh.rows;
   u.cols = (int)sh.cols;
   u.scale = G::kIterScale;
@@ -417,27 +418,22 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   p.rows = p.cols = (int)m;
   p.batch = (int)sh.batch;
   p.ld_out = p.ld_x = ld_p;
-  p.batch_out = p.batch_x = PL * np;
+  p.batch_out = p.batch_x = G::planes(PL) * np;
   p.plane_out = p.plane_x = np;
   p.ld_dev = ld_p;
-  // What rounding takes from the diagonals is kept (gemm::finish) where they are nearly constant: for shorter sides of up
-  // to 64, and of up to 256 in long matrices.  A bf16 result's error is then 1.1 to 1.2 times that of rounding the exact
-  // result; without it up to 1.7 (160 x 6788), but at most 1.35 in the others, where it would cost up to 14 % (16 x 333 x
-  // 130: 92 us without, 106 with).
-  const bool diagonals = PL == 1 && (m <= 64 || (m <= 256 && std::max(sh.rows, sh.cols) >= 4 * m));
-  const auto square = [&](const Square& q) { return Operand{q.at, m, m, ld_p, sh.batch * PL, np}; };
+  const auto square = [&](const Square& q) { return Operand{q.at, m, m, ld_p, sh.batch * G::planes(PL), np}; };
   const auto into = [&](const Square& out, int64_t k) {
     p.k = (int)k;
     p.out = out.at;
-    p.diff_out = diagonals ? out.diff : nullptr;
-    p.quot_out = diagonals ? out.quot : nullptr;
+    p.diff_out = out.diff;
+    p.quot_out = out.quot;
     p.dev_r = p.dev_c = nullptr;
   };
   // out = B(x) with the coefficients of step s; out = x y
   const auto polynomial = [&](const Square& out, const Square& x, int s) {
     into(out, m);
     p.x = x.at;
-    if (diagonals) p.dev_r = p.dev_c = x.diff;
+    p.dev_r = p.dev_c = x.diff;
     p.fa = flat[3 * s];
     p.fb = flat[3 * s + 1];
     p.fc = flat[3 * s + 2];
@@ -445,10 +441,8 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   };
   const auto product = [&](const Square& out, const Square& x, const Square& y) {
     into(out, m);
-    if (diagonals) {
-      p.dev_r = x.quot;
-      p.dev_c = y.quot;
-    }
+    p.dev_r = x.quot;
+    p.dev_c = y.quot;
     return run_sym<G::GRAM, false, PL>(square(x), square(y), p, nsm, st);
   };
   for (int s = 0; s < steps && rc == BCJR_OK;) {
@@ -458,7 +452,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     const bool two = pairing && (left >= 4 || left == 2) && reach[s] * reach[s + 1] <= 15.f;
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
-    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * PL, nx};
+    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * G::planes(PL), nx};
     into(pp, tall ? sh.rows : sh.cols);
     rc = tall ? run_sym<G::GRAM, true, PL>(x, x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, x, p, nsm, st);
     if (rc || (rc = polynomial(bb, pp, s))) break;
@@ -476,17 +470,17 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     q.k = (int)m;
     q.batch = (int)sh.batch;
     q.ld_dev = ld_p;
-    if (diagonals) (tall ? q.dev_r : q.dev_c) = b.quot;
+    (tall ? q.dev_r : q.dev_c) = b.quot;
     if (!end) {
       q.out = x1;
       q.ld_out = ld_x;
-      q.batch_out = PL * nx;
+      q.batch_out = G::planes(PL) * nx;
       q.plane_out = nx;
     }
 #define BCJR_ITER(E) (tall ? run_iter<E, false, PL>(poly, x, q, nsm, st) : run_iter<E, true, PL>(x, poly, q, nsm, st))
     if (!end) {
       rc = BCJR_ITER(G::ITER);
-    } else if constexpr (PL == 1) {
+    } else if constexpr (PL == G::ONE) {
       rc = epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
     } else {
       rc = BCJR_ITER(G::LAST);
@@ -622,9 +616,15 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
   G::Params last{};
   last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one plane of 11 bits leaves an error of about 1e-3, less than bf16's own rounding (1.7e-3); fp16 shows more
-  return out_type == BCJR_BF16 ? run_newton_schulz<1>(sh, u, g_type, steps, coeffs, G::LAST, last, st)
-                               : run_newton_schulz<2>(sh, u, g_type, steps, coeffs, G::LAST, last, st);
+  // One plane of 11 bits leaves an error of about 1e-3, less than bf16's own rounding (1.7e-3); fp16 shows more.
+  // Diagonals are nearly constant (gemm::finish) for shorter sides of up to 64, and of up to 256 in long matrices: a bf16
+  // result's error is 1.1 to 1.2 times that of rounding the exact result with them kept, up to 1.7 without (160 x 6788);
+  // of other shapes at most 1.35 without, where it would cost up to 11 % (16 x 333 x 130: 95 us without, 106 with).
+  const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
+#define BCJR_NS(PL) run_newton_schulz<PL>(sh, u, g_type, steps, coeffs, G::LAST, last, st)
+  if (out_type != BCJR_BF16) return BCJR_NS(G::TWO);
+  return m <= 64 || (m <= 256 && n >= 4 * m) ? BCJR_NS(G::ONE_EXACT) : BCJR_NS(G::ONE);
+#undef BCJR_NS
 }
 
 int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad, float* momentum,
@@ -645,7 +645,7 @@ int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int6
   last.out = w; last.ld_out = ld_w;
   last.keep = (float)(1.0 - (double)lr * (double)weight_decay);
   last.rate = (float)((double)lr * (double)scale);
-  return run_newton_schulz<1>(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
+  return run_newton_schulz<G::ONE>(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

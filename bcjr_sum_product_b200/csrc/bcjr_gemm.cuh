@@ -50,11 +50,18 @@ enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 
 // The iterates are kept as fp16(2^12 x), or for outputs of more than 8 bits as the
 // sum of two such planes (the value and what its rounding left: 22 bits), whose
-// product takes three passes over k: R0 C0 + R0 C1 + R1 C0 (PL below: one plane or
-// two).  2^12:: |x| <= 16 stays finite, and values are
+// product takes three passes over k: R0 C0 + R0 C1 + R1 C0.  2^12:: |x| <= 16 stays finite, and values are
 // rounded to 11 bits down to 2^-26 instead of 2^-14 (the entries of a large
 // matrix of norm 1 are that small).
 constexpr float kIterScale = 4096.f;
+
+// How iterates and Gram matrices are held (PL below).
+enum Planes {
+  ONE = 1,         // one plane
+  TWO = 2,         // two
+  ONE_EXACT = 3    // one, and what rounding took from the diagonals of the symmetric matrices (see finish)
+};
+__host__ __device__ constexpr int planes(int pl) { return pl == TWO ? 2 : 1; }
 
 struct Params {
   int rows, cols, k;         // extents of r, c, k
@@ -72,14 +79,14 @@ struct Params {
   // epilogue
   void* out;
   const __half* x;           // P (POLY), laid out as D
-  // What rounding took from the diagonals of the symmetric matrices (one plane; see finish): of the operands along r
-  // and along c, or null, and of the result.  POLY: the differences; else the quotients.
+  // ONE_EXACT: what rounding took from the diagonals of the operands along r and along c, or null (POLY: the
+  // differences; else the quotients), and from that of the result.
   const float *dev_r, *dev_c;
-  float *diff_out, *quot_out;   // or null
+  float *diff_out, *quot_out;
   int64_t ld_dev;            // from one matrix of the batch to the next
   int64_t ld_out, ld_x;
   int64_t batch_out, batch_x;
-  int64_t plane_out, plane_x;   // PL = 2: from one plane to the other
+  int64_t plane_out, plane_x;   // TWO: from one plane to the other
   int out_type;
   float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
@@ -107,30 +114,30 @@ __device__ __forceinline__ void store_columns(void* out, int64_t at, int64_t ld,
 // (symmetric, so they lie side by side; ld_x is a multiple of 8).
 template <int W, int PL>
 struct Ahead {
-  uint4 h[PL][W / 8];
-  float4 dev[W / 4];         // of the columns
+  uint4 h[planes(PL)][W / 8];
+  float4 dev[PL == ONE_EXACT ? W / 4 : 1];   // of the columns
 };
 template <int EPI, int W, int PL>
 __device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W, PL>& a) {
   if (EPI == POLY && r < p.rows) {
     const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x + c0;
 #pragma unroll
-    for (int l = 0; l < PL; ++l)
+    for (int l = 0; l < planes(PL); ++l)
 #pragma unroll
       for (int i = 0; i < W / 8; ++i)
         a.h[l][i] = c0 + 8 * i < p.cols ? __ldcg(reinterpret_cast<const uint4*>(x + l * p.plane_x + 8 * i)) : make_uint4(0, 0, 0, 0);
   }
-  if (PL == 1 && EPI != OUT && p.dev_c != nullptr) {
+  if (PL == ONE_EXACT && p.dev_c != nullptr) {
     const float* d = p.dev_c + batch * p.ld_dev + c0;
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-      a.dev[i] = c0 + 4 * i < p.cols ? __ldcg(reinterpret_cast<const float4*>(d + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      a.dev[PL == ONE_EXACT ? i : 0] = c0 + 4 * i < p.cols ? __ldcg(reinterpret_cast<const float4*>(d + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 // The row's own deviation.
 template <int EPI, int PL>
 __device__ __forceinline__ float row_deviation(const Params& p, int64_t batch, int r) {
-  if (PL > 1 || EPI == OUT || p.dev_r == nullptr || r >= p.rows) return EPI == POLY ? 0.f : 1.f;
+  if (PL != ONE_EXACT || p.dev_r == nullptr || r >= p.rows) return EPI == POLY ? 0.f : 1.f;
   return __ldcg(p.dev_r + batch * p.ld_dev + r);
 }
 
@@ -138,7 +145,7 @@ __device__ __forceinline__ float row_deviation(const Params& p, int64_t batch, i
 //
 // The diagonals of the symmetric matrices of a small or long X are nearly constant, so their roundings to 11 bits all
 // go the same way, and a few steps of that are an error of 2.4e-3 (160 x 6788) where independent roundings leave
-// 0.8e-3.  Where `diff_out` and the others are given, what rounding took from a diagonal is therefore kept in fp32: as a
+// 0.8e-3.  With ONE_EXACT what rounding took from a diagonal is therefore kept in fp32: as a
 // difference d, with which P^2 is
 // (P16^2)_rc + P_rc (d_r + d_c) to first order, and as a quotient, by which the rows and columns of the other
 // products are multiplied (right for the diagonal's part of the sum, and nothing next to the rest's own rounding).
@@ -151,7 +158,7 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
   const float unit = EPI == OUT ? p.fa : EPI == LAST ? 1.f / (kIterScale * kIterScale) : 1.f / kIterScale;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] *= unit;
-  if constexpr (PL == 1 && EPI != OUT && EPI != POLY) {
+  if constexpr (PL == ONE_EXACT && EPI != POLY) {
     if (p.dev_c != nullptr) {
       const float* d = reinterpret_cast<const float*>(a.dev);
 #pragma unroll
@@ -171,11 +178,11 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
     if constexpr (EPI == POLY) {
       const __half* x = reinterpret_cast<const __half*>(a.h);   // W values, then what they left
       const float* d = reinterpret_cast<const float*>(a.dev);
-      const float on_diagonal = fmaf(p.fa, kIterScale, PL == 1 ? p.fb * dev_row : 0.f);
+      const float on_diagonal = fmaf(p.fa, kIterScale, PL == ONE_EXACT ? p.fb * dev_row : 0.f);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const float pv = PL > 1 ? __half2float(x[i]) + __half2float(x[(PL - 1) * W + i]) : __half2float(x[i]);
-        if (PL == 1 && p.dev_c != nullptr) v[i] = fmaf(pv * (1.f / kIterScale), dev_row + d[i], v[i]);
+        const float pv = PL == TWO ? __half2float(x[i]) + __half2float(x[(planes(PL) - 1) * W + i]) : __half2float(x[i]);
+        if (PL == ONE_EXACT) v[i] = fmaf(pv * (1.f / kIterScale), dev_row + d[i], v[i]);
         v[i] = fmaf(p.fb, pv, p.fc * v[i]);
       }
       if (diagonal) {
@@ -185,7 +192,7 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
     }
     // (as a sum of products with 0 and 1: a selection becomes an index into local memory)
     float exact = 0.f;
-    const bool keep = PL == 1 && EPI != ITER && diagonal && p.diff_out != nullptr;
+    const bool keep = PL == ONE_EXACT && EPI != ITER && diagonal;
     if (keep) {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -194,12 +201,12 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
       }
     }
 #pragma unroll
-    for (int plane = 0; plane < PL; ++plane) {
+    for (int plane = 0; plane < planes(PL); ++plane) {
       alignas(16) __half h[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         h[i] = __float2half_rn(v[i]);
-        if (PL > 1) v[i] -= __half2float(h[i]);
+        if (PL == TWO) v[i] -= __half2float(h[i]);
       }
       if (keep && (unsigned)(r - c0) < (unsigned)W) {
         const float back = __half2float(__float2half_rn(exact));
@@ -268,10 +275,10 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, int64_t ld, int s
 // first value of k, the third coordinates of R and C in their maps.
 template <int KIND, int PL>
 __device__ __forceinline__ void block_place(int kb, int blocks, int batch, int* k, int* zr, int* zc) {
-  const int pass = PL == 1 || kb < blocks ? 0 : kb < 2 * blocks ? 1 : 2;
+  const int pass = PL != TWO || kb < blocks ? 0 : kb < 2 * blocks ? 1 : 2;
   *k = (kb - pass * blocks) * (KIND == MX ? 128 : 64);
-  *zr = batch * PL + (pass == 2 ? 1 : 0);
-  *zc = batch * PL + (pass == 1 ? 1 : 0);
+  *zr = batch * planes(PL) + (pass == 2 ? 1 : 0);
+  *zc = batch * planes(PL) + (pass == 1 ? 1 : 0);
 }
 
 // Tile t of a symmetric product of TR-row and TC-column tiles: row tile j has the
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   }
   const int r0 = tr * kRowsTile, c0 = tcn * BN;
   const int blocks = (p.k + kElems - 1) / kElems;
-  const int total = PL > 1 ? 3 * blocks : blocks;
+  const int total = PL == TWO ? 3 * blocks : blocks;
   const int kb0 = (int)((int64_t)total * rank / p.splits), kb1 = (int)((int64_t)total * (rank + 1) / p.splits);
 
   if (threadIdx.x == 0) {
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int all = p.tiles * p.batch;
   const int blocks = (p.k + kElems - 1) / kElems;   // > 0
-  const int total = PL > 1 ? 3 * blocks : blocks;
+  const int total = PL == TWO ? 3 * blocks : blocks;
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_r);
