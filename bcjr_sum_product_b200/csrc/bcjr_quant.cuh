@@ -108,6 +108,9 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 // shared memory (cp.async, each thread fetching just what it will read, so no
 // barrier guards them) while this one is worked on and stored.
 // ROW_BLOCKS: one scale for each row (or column) and 128 values; else one for the tile.
+// 8192 x 8192 fp32 minus fp32 to both layouts: 105 to 113 us, 6.0 to 6.4 TB/s of the
+// measured 6.57 (without PIPE 148 us: between a tile's loads and its stores its SM
+// asked for nothing).  4003 x 2048 bf16 to both: 12 us, a tile's own latency twice.
 template <int T, bool E5M2, bool ROW_BLOCKS, bool PIPE>
 __global__ void __launch_bounds__(kThreads, 2) quantise_kernel(const QuantParams p) {
   constexpr int TOP = E5M2 ? 16 : 9;
