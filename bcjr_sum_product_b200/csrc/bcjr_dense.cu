@@ -517,12 +517,12 @@ int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int gri
   return BCJR_OK;
 }
 
-// From four rounds of tiles on, blocks stay (as many as fit the SMs: two, or one where
-// both x and minus are fetched ahead) and fetch ahead.
+// From four rounds of tiles on, blocks stay (two to an SM, or one where both x and minus, 96 to
+// 128 KB of a tile, are fetched ahead) and fetch ahead.
 template <int T>
 int run_quantise(Q::QuantParams p, bool e5m2, bool row_blocks, int nsm, cudaStream_t st) {
   if (p.vec && p.tiles > 4 * nsm)
-    return launch_quantise<T, true>(p, e5m2, row_blocks, p.minus != nullptr && T == Q::IN_F32 ? nsm : 2 * nsm, st);
+    return launch_quantise<T, true>(p, e5m2, row_blocks, p.minus != nullptr ? nsm : 2 * nsm, st);
   return launch_quantise<T, false>(p, e5m2, row_blocks, p.tiles, st);
 }
 

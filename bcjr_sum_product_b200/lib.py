@@ -392,7 +392,7 @@ def _fp8_matmul(args_a, args_b, M, N, K, alpha, out_dtype, out, device, st):
         out, ld = _empty((M, N), (N, 1), dtype=out_dtype, device=device), N
     else:
         out_dtype, ld = out.dtype, _ld(out)
-    rc = load().bcjr_fp8_matmul(*args_a, *args_b, M, N, K, alpha, out.data_ptr(), _TYPES[out_dtype], ld, st)
+    rc = load().bcjr_fp8_matmul(*args_a, *args_b, M, N, K, float(alpha), out.data_ptr(), _TYPES[out_dtype], ld, st)
     _check(rc, "bcjr_fp8_matmul")
     return out
 
@@ -429,7 +429,7 @@ def _orthogonalise(g, steps, coeffs, eps, out_dtype, st):
     rows, cols = g.shape[-2:]
     out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
     batch, stride = (g.shape[0], g.stride(0)) if g.dim() == 3 else (1, 0)
-    rc = load().bcjr_orthogonalise(g.data_ptr(), _TYPES[g.dtype], batch, rows, cols, _ld(g), stride, steps, coeffs, eps,
+    rc = load().bcjr_orthogonalise(g.data_ptr(), _TYPES[g.dtype], batch, rows, cols, _ld(g), stride, steps, coeffs, float(eps),
                                    out.data_ptr(), _TYPES[out_dtype], cols, rows * cols, st)
     _check(rc, "bcjr_orthogonalise")
     return out
@@ -458,6 +458,7 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: f
 def _muon_step(w, grad, momentum, lr, mu, nesterov, weight_decay, scale, steps, coeffs, eps, st):
     rows, cols = w.shape
     rc = load().bcjr_muon_step(w.data_ptr(), _ld(w), grad.data_ptr(), _TYPES[grad.dtype], _ld(grad), momentum.data_ptr(),
-                               _ld(momentum), rows, cols, lr, mu, nesterov, weight_decay, scale, steps, coeffs, eps, st)
+                               _ld(momentum), rows, cols, float(lr), float(mu), nesterov, float(weight_decay), float(scale), steps,
+                               coeffs, float(eps), st)
     _check(rc, "bcjr_muon_step")
     return w, momentum

@@ -96,7 +96,7 @@ def run(w_target: torch.Tensor, codebook: torch.Tensor, L: int, k: int, V: int, 
     if stream is not None:
         # everything of the run, allocations included, on that stream, after the caller's and before its next
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=w_target.device)
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=w_target.device)
         caller = torch.cuda.current_stream(w_target.device)
         stream.wait_stream(caller)
         with torch.cuda.stream(stream):

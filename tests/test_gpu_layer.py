@@ -208,6 +208,18 @@ def test_matmul_padding_is_not_read():
     assert (room[m:] == 7).all() and (room[:, :3] == 7).all() and (room[:, 3 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("up,down", [(100, -100), (-110, 110), (60, 10)])
+@pytest.mark.parametrize("m,n", [(20, 150), (2048, 2400)])
+def test_matmul_scales_of_any_size(up, down, m, n):
+    """Scales far from one another: powers of two on the operands are the same powers on
+    the result."""
+    x, w = randn(m, 300, seed=36).to(DEV), randn(n, 300, seed=37).to(DEV)
+    plain = lib.fp8_matmul(*lib.fp8_quantise(x), *lib.fp8_quantise(w, 128), out_dtype=torch.float32)
+    far = lib.fp8_matmul(*lib.fp8_quantise(x * 2.0 ** up), *lib.fp8_quantise(w * 2.0 ** down, 128), out_dtype=torch.float32)
+    finished()
+    assert torch.equal(far, plain * 2.0 ** (up + down))
+
+
 def test_matmul_not_finite_values_stay_in_their_rows():
     x, w = randn(40, 300, seed=19), randn(140, 300, seed=20)
     x[5, 3] = math.nan

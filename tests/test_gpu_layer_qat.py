@@ -4,6 +4,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -204,6 +205,29 @@ def test_streams_at_once():
             with torch.cuda.stream(s):
                 x = x.clone()
                 got.append(bits(chain(x, w, torch.zeros_like(x))))
+    finished()
+    assert same(got[0], want[0]) and same(got[1], want[1])
+
+
+def test_two_host_threads():
+    want, data = [], [cases(8), cases(9)]
+    for x, w in data:
+        want.append(bits(chain(x.clone(), w, torch.zeros_like(x))))
+    finished()
+    got = [None, None]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                x = data[i][0].clone()
+                got[i] = bits(chain(x, data[i][1], torch.zeros_like(x)))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
     finished()
     assert same(got[0], want[0]) and same(got[1], want[1])
 
