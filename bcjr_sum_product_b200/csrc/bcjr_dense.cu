@@ -129,11 +129,11 @@ int allow_smem(const void* kern, std::atomic<uint64_t>* done, int smem) {
   return BCJR_OK;
 }
 
-// `chained`: the call's own earlier kernel precedes this one on the stream, whose
-// set-up may then overlap that one's end (both kernels wait for it before they touch
-// its results).
+// Dependent launch: this kernel's set-up may overlap the end of the kernel before it on
+// the stream, where that one allows it (the library's own do); it waits for that one
+// before it touches memory.
 template <class Kern>
-int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cluster, bool chained, const CUtensorMap& mr,
+int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cluster, const CUtensorMap& mr,
            const CUtensorMap& mc, const G::Params& p, cudaStream_t st) {
   if (grid > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
   cudaLaunchAttribute attr[2];
@@ -149,7 +149,7 @@ int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cl
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = chained ? 2 : 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, mr, mc, p) != cudaSuccess) {
     cudaGetLastError();
     return BCJR_ERR_CUDA;
@@ -159,7 +159,7 @@ int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cl
 }
 
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
-int launch_tile(const Operand& r, const Operand& c, const G::Params& p, bool chained, cudaStream_t st) {
+int launch_tile(const Operand& r, const Operand& c, const G::Params& p, cudaStream_t st) {
   using S = G::TileShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
   static std::atomic<uint64_t> done{0};
@@ -168,11 +168,11 @@ int launch_tile(const Operand& r, const Operand& c, const G::Params& p, bool cha
   if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN))) return rc;
   auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI, PL>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
-  return launch(kern, (int64_t)p.tiles * p.splits, p.batch, G::kTileThreads, S::kSmem, p.splits, chained, mr, mc, p, st);
+  return launch(kern, (int64_t)p.tiles * p.splits, p.batch, G::kTileThreads, S::kSmem, p.splits, mr, mc, p, st);
 }
 
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
-int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm, bool chained, cudaStream_t st) {
+int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   using S = G::PairShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
   static std::atomic<uint64_t> done{0};
@@ -187,7 +187,7 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   // with k = 2048, where R is 16 MB, bands cost 3 %).
   G::Params pb = p;
   pb.band = r.inner * r.outer * elem > ((int64_t)48 << 20) ? std::min(p.tiles_r, 16) : p.tiles_r;
-  return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, chained, mr, mc, pb, st);
+  return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, mr, mc, pb, st);
 }
 
 // Blocks of one tile: as many (1, 2, 4 or 8) as the tiles leave room for, each with at least four stages of k.  Exchanging
@@ -208,7 +208,7 @@ int matmul_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)tiles;
   p.splits = splits_for(tiles, parts(p.k, 128), nsm);
-  return launch_tile<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, false, st);
+  return launch_tile<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, st);
 }
 template <int BN>
 int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
@@ -216,7 +216,7 @@ int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   if (tiles > INT32_MAX / 2) return BCJR_ERR_UNSUPPORTED;
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)tiles;
-  return launch_pair<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, nsm, false, st);
+  return launch_pair<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, nsm, st);
 }
 
 int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
@@ -226,18 +226,33 @@ int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st)
   if (p.cols <= 16) return matmul_tile<16>(r, c, p, nsm, st);
   if (p.cols <= 32) return matmul_tile<32>(r, c, p, nsm, st);
   if (p.cols <= 64) return matmul_tile<64>(r, c, p, nsm, st);
-  // Pairs: the width of tile whose rounds over the GPU take least, from measured times: `block` for 128 values of k
-  // and `end` for what a tile's stores add (256 columns leave room for one set of sums only, so their stores do not
-  // overlap the next tile's products).  8192 x 8192 x 2048: 128 / 224 / 256 columns 160 / 122 / 132 us;
-  // 2048 x 2048 x 8192 (one round of 256, two of 224): 44 / 49 / 32 us.
-  const int64_t pairs = nsm / 2, rows = parts(p.rows, 256), blocks = parts(p.k, 128);
-  const auto cost = [&](int width, double block, double end) {
-    return (double)parts(rows * parts(p.cols, width), pairs) * (blocks * block + end);
+  // More columns: the kernel and tile width whose estimated time in us is least.  The estimates are fitted to measured
+  // times (100 to 8192 x 512 to 8192 x 512 to 8192); what they choose is within a tenth of the best of the five almost
+  // everywhere.  For pairs: rounds over the GPU, each of `block` for 128 values of k and `end`, but at least as long as
+  // its stores (256 columns leave room for one set of sums only, whose stores overlap nothing).  For single blocks: rounds
+  // of two blocks an SM, `block` shared by the blocks of an SM, and the exchange of sums where k is split.
+  // 8192 x 8192 x 2048: pairs of 128 / 224 / 256 columns 160 / 122 / 132 us; 2048 x 2048 x 8192: 44 / 49 / 32;
+  // 400 x 2048 x 512: single blocks of 64 / 128 columns 5.7 / 6.6, pairs 8.6 / 10.8 / 11.4; 200 x 2048 x 8192: 16.4 / 12.8,
+  // pairs 23 / 28 / 29.
+  const int64_t pairs = nsm / 2, rows2 = parts(p.rows, 256), rows = parts(p.rows, 128), blocks = parts(p.k, 128);
+  const auto pair = [&](int width, double block, double end, double stores) {
+    return 4.0 + (double)parts(rows2 * parts(p.cols, width), pairs) * std::max(blocks * block + end, stores);
   };
-  const double c128 = cost(128, 0.33, 0.4), c224 = cost(224, 0.435, 0.6), c256 = cost(256, 0.45, 2.2);
-  if (rows * parts(p.cols, 128) * 4 < nsm) return matmul_tile<128>(r, c, p, nsm, st);
-  if (c256 <= c224 && c256 <= c128) return matmul_pair<256>(r, c, p, nsm, st);
-  return c224 <= c128 ? matmul_pair<224>(r, c, p, nsm, st) : matmul_pair<128>(r, c, p, nsm, st);
+  const auto single = [&](int width, double begin, double block, double exchange) {
+    const int64_t tiles = rows * parts(p.cols, width);
+    const int s = splits_for(tiles, blocks, nsm);
+    return begin * (double)parts(tiles * s, 2 * nsm) + std::max(1.0, (double)(tiles * s) / nsm) * (double)parts(blocks, s) * block +
+           (s > 1 ? exchange : 0.0);
+  };
+  const double cost[5] = {single(64, 5.3, 0.30, 1.4), single(128, 5.8, 0.38, 3.5), pair(128, 0.33, 0.4, 2.9),
+                          pair(224, 0.435, 0.6, 4.6), pair(256, 0.45, 3.5, 0.0)};
+  switch (std::min_element(cost, cost + 5) - cost) {
+    case 0: return matmul_tile<64>(r, c, p, nsm, st);
+    case 1: return matmul_tile<128>(r, c, p, nsm, st);
+    case 2: return matmul_pair<128>(r, c, p, nsm, st);
+    case 3: return matmul_pair<224>(r, c, p, nsm, st);
+    default: return matmul_pair<256>(r, c, p, nsm, st);
+  }
 }
 
 // ------------------------------------------------------------ Newton-Schulz
@@ -284,14 +299,14 @@ int sym_tile(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStrea
   const int64_t t = parts(p.rows, G::kRowsTile);
   p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
   p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
-  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, y, p, true, st);
+  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, y, p, st);
 }
 template <int BN, int EPI, bool MN, int PL>
 int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, 2 * G::kRowsTile);
   p.tiles_r = (int)t;
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
-  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, y, p, nsm, true, st);
+  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, y, p, nsm, st);
 }
 template <int EPI, bool MN, int PL>
 int run_sym(const Operand& x, const Operand& y, const G::Params& p, int nsm, cudaStream_t st) {
@@ -307,13 +322,13 @@ int iter_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStre
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
   p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
-  return launch_tile<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, true, st);
+  return launch_tile<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, st);
 }
 template <int BN, int EPI, bool R_MN, int PL>
 int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  return launch_pair<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, nsm, true, st);
+  return launch_pair<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, nsm, st);
 }
 template <int EPI, bool R_MN, int PL>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
@@ -344,8 +359,8 @@ int launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
   cfg.blockDim = dim3(Q::kUpdateThreads, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, Q::norm_kernel<T>, u);
   cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, Q::norm_kernel<T>, u);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, Q::start_kernel<T>, u);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -509,6 +524,11 @@ int launch_quantise(const Q::QuantParams& p, bool e5m2, bool row_blocks, int gri
   cfg.blockDim = dim3(Q::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     cudaGetLastError();
     return BCJR_ERR_CUDA;

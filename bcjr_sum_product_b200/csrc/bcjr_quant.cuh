@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, 2) quantise_kernel(const QuantParams
   extern __shared__ __align__(16) uint8_t fetched[];   // PIPE: [8 rows][512 threads] of 4 values of x, then of minus
   __shared__ alignas(16) uint32_t most[16][kTile];
   __shared__ uint32_t words[kTile][32];
+  tc::launch_dependents();
+  tc::wait_for_earlier();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* mine = fetched + threadIdx.x * kBytes;
   uint8_t* mine_minus = fetched + kRows * kThreads * kBytes + threadIdx.x * 16;
@@ -348,6 +350,7 @@ __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams
   using X = typename In<T>::type;
   __shared__ double part[8];
   tc::launch_dependents();
+  tc::wait_for_earlier();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int spans = (p.cols + kSpan - 1) / kSpan;
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
