@@ -336,7 +336,7 @@ struct TileShape {
 // the order of the ranks, so the result does not depend on timing.  What bounds it
 // is latency, not a pipe: of the 6 us of a product of 512 x 512 x 2048 the first
 // copy takes 0.8, eight stages 1.7 (64 bytes a clock and SM from L2), the exchange
-// 2.0, the stores 0.9.  One token through 8192 x 2048 (17 MB): 7.4 us, 2.3 TB/s.
+// 2.0, the stores 0.9.  One token through 8192 x 2048 (17 MB): 6.5 us, 2.6 TB/s.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
 __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
                                                              const __grid_constant__ CUtensorMap map_c, const Params p) {
