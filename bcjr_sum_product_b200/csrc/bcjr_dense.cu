@@ -342,8 +342,10 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
 // one Gram matrix of X and one product with X instead of two, for three more products of the shorter side's size.
 // Estimated from measured times: 5 us for each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s for Gram
 // matrices (whole flops), products with X and small symmetric products.  Not for three or more steps at once: the
-// error of P grows with every step that does not take it from X itself (two steps: as one at a time, 1e-3).
+// error of P grows with every step that does not take it from X itself (two steps: as one at a time, 1e-3, from 512
+// rows on; 16 x 3652: 2.3e-3 against 1.1e-3, so not for batches of small matrices either).
 bool worth_pairing(const Shape2& sh) {
+  if (std::min(sh.rows, sh.cols) < 512) return false;
   const double m = (double)std::min(sh.rows, sh.cols), n = (double)std::max(sh.rows, sh.cols), b = (double)sh.batch;
   const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 2 / 1.6e15);
   return saved > 1.1 * 3.0 * (5.0 + 1e6 * b * m * m * m / 0.9e15);

@@ -145,9 +145,8 @@ __device__ __forceinline__ float row_deviation(const Params& p, int64_t batch, i
 //
 // The diagonals of the symmetric matrices of a small or long X are nearly constant, so their roundings to 11 bits all
 // go the same way, and a few steps of that are an error of 2.4e-3 (160 x 6788) where independent roundings leave
-// 0.8e-3.  With ONE_EXACT what rounding took from a diagonal is therefore kept in fp32: as a
-// difference d, with which P^2 is
-// (P16^2)_rc + P_rc (d_r + d_c) to first order, and as a quotient, by which the rows and columns of the other
+// 0.8e-3.  With ONE_EXACT what rounding took from a diagonal is therefore kept in fp32: as a difference d, with which
+// P^2 is (P16^2)_rc + P_rc (d_r + d_c) to first order, and as a quotient, by which the rows and columns of the other
 // products are multiplied (right for the diagonal's part of the sum, and nothing next to the rest's own rounding).
 template <int EPI, int W, int PL>
 __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, float dev_row,
