@@ -308,10 +308,16 @@ int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStrea
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
   return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, y, p, nsm, st);
 }
+// Pairs of SMs (tiles of 256 rows) where they have a quarter of the GPU's SMs' number of tiles to work on: from half of
+// that on 1024^2 takes 130 us instead of 108, with twice of it 2048^2 takes 245 instead of 216.  Never for matrices of at
+// most 128 rows, where half of every such tile is empty: 256 of 128 x 256 take 185 us in single blocks and 321 in pairs,
+// 1000 of 32 x 96 394 and 680; from 129 rows on pairs win (64 of 256 x 512: 171 us against 193).  Single blocks take 64
+// columns where those fill two blocks an SM at most (16 of 333 x 130: 86 us, at one block an SM 96), else 128 (256 of
+// 128 x 256: 185 us against 224).
 template <int EPI, bool MN, int PL>
 int run_sym(const Operand& x, const Operand& y, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, y, p, nsm, st);
+  if (p.rows > G::kRowsTile && t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, y, p, nsm, st);
   if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN, PL>(x, y, p, nsm, st);
   return sym_tile<128, EPI, MN, PL>(x, y, p, nsm, st);
 }
@@ -330,10 +336,13 @@ int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStre
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
   return launch_pair<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, nsm, st);
 }
+// As for the symmetric products: pairs from a quarter (1024 x 2048: 135 us; from a tenth 141; 1024 x 4096 from a half:
+// 196 instead of 163), and not for 128 rows or fewer (1000 of 32 x 96: 394 us against 420, 64 of 128 x 128: 68 against 77).
 template <int EPI, bool R_MN, int PL>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (t2 * parts(p.cols, 256) * p.batch * 4 >= nsm) return iter_pair<256, EPI, R_MN, PL>(r, c, p, nsm, st);
+  if (p.rows > G::kRowsTile && t2 * parts(p.cols, 256) * p.batch * 4 >= nsm)
+    return iter_pair<256, EPI, R_MN, PL>(r, c, p, nsm, st);
   if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN, PL>(r, c, p, nsm, st);
   return iter_tile<128, EPI, R_MN, PL>(r, c, p, nsm, st);
 }

@@ -326,6 +326,17 @@ def test_orthogonalise_roundings_do_not_add_up(rows, cols):
     assert rel <= 2.5e-3
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(64, 128, 128), (200, 128, 250), (40, 130, 900), (40, 700, 100), (300, 32, 96),
+                                             (500, 17, 9), (1000, 1, 3), (37, 129, 129)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_orthogonalise_many_small_matrices(batch, rows, cols, dtype):
+    """Batches large enough for every kernel that the tile rule knows, on both sides of 128 rows."""
+    g = randn(batch, rows, cols, seed=31).to(dtype)
+    out = lib.orthogonalise(g.to(DEV))
+    finished()
+    check_orthogonal(out, g)
+
+
 def test_orthogonalise_batch_strides_and_zeros():
     g = randn(5, 60, 200, seed=22).to(DEV)
     g[2] = 0
