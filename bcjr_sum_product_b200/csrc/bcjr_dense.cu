@@ -158,7 +158,7 @@ int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cl
   return BCJR_OK;
 }
 
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 int launch_tile(const Operand& r, const Operand& c, const G::Params& p, cudaStream_t st) {
   using S = G::TileShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
@@ -166,12 +166,12 @@ int launch_tile(const Operand& r, const Operand& c, const G::Params& p, cudaStre
   CUtensorMap mr, mc;
   int rc;
   if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN))) return rc;
-  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI, PL>;
+  auto kern = G::tile_kernel<KIND, BN, R_MN, C_MN, EPI>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   return launch(kern, (int64_t)p.tiles * p.splits, p.batch, G::kTileThreads, S::kSmem, p.splits, mr, mc, p, st);
 }
 
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   using S = G::PairShape<KIND, BN>;
   constexpr int elem = KIND == G::MX ? 1 : 2;
@@ -179,7 +179,7 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   CUtensorMap mr, mc;
   int rc;
   if ((rc = make_map(&mr, r, elem, R_MN ? 64 : G::kRowsTile)) || (rc = make_map(&mc, c, elem, C_MN ? 64 : BN / 2))) return rc;
-  auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI, PL>;
+  auto kern = G::pair_kernel<KIND, BN, R_MN, C_MN, EPI>;
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
   // The pairs that run together work on neighbouring columns of all of R, which then has to stay in
@@ -208,7 +208,7 @@ int matmul_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)tiles;
   p.splits = splits_for(tiles, parts(p.k, 128), nsm);
-  return launch_tile<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, st);
+  return launch_tile<G::MX, BN, false, false, G::OUT>(r, c, p, st);
 }
 template <int BN>
 int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
@@ -216,13 +216,13 @@ int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
   if (tiles > INT32_MAX / 2) return BCJR_ERR_UNSUPPORTED;
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)tiles;
-  return launch_pair<G::MX, BN, false, false, G::OUT, G::ONE>(r, c, p, nsm, st);
+  return launch_pair<G::MX, BN, false, false, G::OUT>(r, c, p, nsm, st);
 }
 
 int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
   int nsm = 0;
   if (int rc = sm_count(&nsm)) return rc;
-  p.batch = 1;
+  p.batch = p.planes = 1;
   if (p.cols <= 16) return matmul_tile<16>(r, c, p, nsm, st);
   if (p.cols <= 32) return matmul_tile<32>(r, c, p, nsm, st);
   if (p.cols <= 64) return matmul_tile<64>(r, c, p, nsm, st);
@@ -262,7 +262,8 @@ constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 // The iterates and polynomials are kept in fp16 with headroom for entries up to
 // 16; the singular values of u / |u| lie in [0, 1].  False if, sampled over the
 // interval that each step can reach, the coefficients drive a singular value
-// above 2 or |a + b t + c t^2| above 8.  `reach`: the largest of the latter for each step.
+// above 2 or |a + b t + c t^2| above 8.  `reach`: the largest of the latter for each step,
+// by which the step can amplify what an earlier one left in X.
 bool coeffs_bounded(const float* co, int steps, float* reach) {
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
@@ -292,21 +293,26 @@ int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps)
   return BCJR_OK;
 }
 
+// Stages of k of one product of iterates, but for those of a diagonal.
+int64_t stages_of(const G::Params& p) {
+  return parts(p.k, 64) * (1 + (p.second_r == G::ALL) + (p.second_c == G::ALL));
+}
+
 // Symmetric products x y^T: P = X X^T (or X^T X), B = a I + b P + c P^2, and products of such matrices with one
 // another (polynomials of one matrix commute), tiles up to the diagonal.
-template <int BN, int EPI, bool MN, int PL>
+template <int BN, int EPI, bool MN>
 int sym_tile(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile);
   p.tiles = (int)((G::kRowsTile / BN) * t * (t + 1) / 2);
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
-  return launch_tile<G::F16, BN, MN, MN, EPI, PL>(x, y, p, st);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, stages_of(p), nsm);
+  return launch_tile<G::F16, BN, MN, MN, EPI>(x, y, p, st);
 }
-template <int BN, int EPI, bool MN, int PL>
+template <int BN, int EPI, bool MN>
 int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, 2 * G::kRowsTile);
   p.tiles_r = (int)t;
   p.tiles = (int)((2 * G::kRowsTile / BN) * t * (t + 1) / 2);
-  return launch_pair<G::F16, BN, MN, MN, EPI, PL>(x, y, p, nsm, st);
+  return launch_pair<G::F16, BN, MN, MN, EPI>(x, y, p, nsm, st);
 }
 // Pairs of SMs (tiles of 256 rows) where they have a quarter of the GPU's SMs' number of tiles to work on: from half of
 // that on 1024^2 takes 130 us instead of 108, with twice of it 2048^2 takes 245 instead of 216.  Never for matrices of at
@@ -314,49 +320,51 @@ int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStrea
 // 1000 of 32 x 96 394 and 680; from 129 rows on pairs win (64 of 256 x 512: 171 us against 193).  Single blocks take 64
 // columns where those fill two blocks an SM at most (16 of 333 x 130: 86 us, at one block an SM 96), else 128 (256 of
 // 128 x 256: 185 us against 224).
-template <int EPI, bool MN, int PL>
+template <int EPI, bool MN>
 int run_sym(const Operand& x, const Operand& y, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
-  if (p.rows > G::kRowsTile && t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN, PL>(x, y, p, nsm, st);
-  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN, PL>(x, y, p, nsm, st);
-  return sym_tile<128, EPI, MN, PL>(x, y, p, nsm, st);
+  if (p.rows > G::kRowsTile && t2 * (t2 + 1) * p.batch * 4 >= nsm) return sym_pair<128, EPI, MN>(x, y, p, nsm, st);
+  if (t * (t + 1) * p.batch <= 2 * nsm) return sym_tile<64, EPI, MN>(x, y, p, nsm, st);
+  return sym_tile<128, EPI, MN>(x, y, p, nsm, st);
 }
 
 // X' = B X (or X B).
-template <int BN, int EPI, bool R_MN, int PL>
+template <int BN, int EPI, bool R_MN>
 int iter_tile(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  p.splits = splits_for((int64_t)p.tiles * p.batch, parts(p.k, 64) * (PL == G::TWO ? 3 : 1), nsm);
-  return launch_tile<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, st);
+  p.splits = splits_for((int64_t)p.tiles * p.batch, stages_of(p), nsm);
+  return launch_tile<G::F16, BN, R_MN, false, EPI>(r, c, p, st);
 }
-template <int BN, int EPI, bool R_MN, int PL>
+template <int BN, int EPI, bool R_MN>
 int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStream_t st) {
   p.tiles_r = (int)parts(p.rows, 2 * G::kRowsTile);
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
-  return launch_pair<G::F16, BN, R_MN, false, EPI, PL>(r, c, p, nsm, st);
+  return launch_pair<G::F16, BN, R_MN, false, EPI>(r, c, p, nsm, st);
 }
 // As for the symmetric products: pairs from a quarter (1024 x 2048: 135 us; from a tenth 141; 1024 x 4096 from a half:
 // 196 instead of 163), and not for 128 rows or fewer (1000 of 32 x 96: 394 us against 420, 64 of 128 x 128: 68 against 77).
-template <int EPI, bool R_MN, int PL>
+template <int EPI, bool R_MN>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
   if (p.rows > G::kRowsTile && t2 * parts(p.cols, 256) * p.batch * 4 >= nsm)
-    return iter_pair<256, EPI, R_MN, PL>(r, c, p, nsm, st);
-  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN, PL>(r, c, p, nsm, st);
-  return iter_tile<128, EPI, R_MN, PL>(r, c, p, nsm, st);
+    return iter_pair<256, EPI, R_MN>(r, c, p, nsm, st);
+  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
+  return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
 }
 
-// Whether two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
-// one Gram matrix of X and one product with X instead of two, for three more products of the shorter side's size.
-// Estimated from measured times: 5 us for each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s for Gram
-// matrices (whole flops), products with X and small symmetric products.  Not for three or more steps at once: the
-// error of P grows with every step that does not take it from X itself (two steps: as one at a time, 1e-3, from 512
-// rows on; 16 x 3652: 2.3e-3 against 1.1e-3, so not for batches of small matrices either).
+// Whether the first two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
+// one Gram matrix of X and one product with X (two passes) instead of two, for three more products of the shorter
+// side's size.  Estimated from measured times: 5 us for each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s
+// for Gram matrices (whole flops), products with X and small symmetric products.
+// Only the first two, and from 512 rows on.  A rounding N of P turns a direction of eigenvalue t into others by
+// |N u| (f(t) - f(0)) / t, with f = B2 B1 from 11.9 at t = 0 to 0.5 at t = 1.  |N u| is about 2^-12 t sqrt(rank / m), and
+// at first t is at most 1 / rank: next to nothing (512 rows or more: as one step at a time; 16 x 3652: 2.3e-3 against
+// 1.1e-3).  Later every t is near 1: the last two steps at once made results of rank 256 of 1536 x 6145 wrong by 6e-3.
 bool worth_pairing(const Shape2& sh) {
   if (std::min(sh.rows, sh.cols) < 512) return false;
   const double m = (double)std::min(sh.rows, sh.cols), n = (double)std::max(sh.rows, sh.cols), b = (double)sh.batch;
-  const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 2 / 1.6e15);
+  const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 4 / 1.6e15);
   return saved > 1.1 * 3.0 * (5.0 + 1e6 * b * m * m * m / 0.9e15);
 }
 
@@ -381,10 +389,9 @@ int launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
   return BCJR_OK;
 }
 
-// The whole iteration, with iterates held as PL says; `last` holds the epilogue of the last product (out, its
-// layout and type, the weights' factors) and says which by `epi`.
-template <int PL>
-int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi,
+// The whole iteration; `last` holds the epilogue of the last product (out, its layout and type, the weights'
+// factors) and says which by `epi`.  `precise`: every product with all second planes, for a result of more than 8 bits.
+int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi, bool precise,
                       const G::Params& last, cudaStream_t st) {
   int nsm = 0;
   if (int rc = sm_count(&nsm)) return rc;
@@ -395,27 +402,29 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   // warps take 512 columns of a row at a time; enough blocks of eight warps for every SM four times over
   const int64_t items = sh.rows * parts(sh.cols, Q::kSpan);
   u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
-  __half *x0, *x1;
-  struct Square {           // a symmetric matrix and what rounding took from its diagonal
-    __half* at;
-    float *diff, *quot;
-  } pp{}, bb{}, tt{};
-  double* partial;
   const bool pairing = steps > 1 && worth_pairing(sh);
   float flat[3 * kMaxSteps], reach[kMaxSteps];
   for (int i = 0; i < 3 * steps; ++i) flat[i] = coeffs != nullptr ? coeffs[i] : kMuonCoeffs[i % 3];
   coeffs_bounded(flat, steps, reach);
+  // The product with X_s reads its second plane unless what one plane leaves out can grow at most four times in the steps
+  // that are left (Muon's last step: 3.4): a result of rank 1, 512 x 512, is off by 0.2e-3 with both planes in all five
+  // steps, 1.1e-3 in all but the last, 2.6e-3 in all but the last two, 0.15 in none.
+  bool both[kMaxSteps];
+  double gain = 1.0;
+  for (int s = steps - 1; s >= 0; --s) {
+    gain *= reach[s];
+    both[s] = precise || gain > 4.0;
+  }
+  const G::Second squares = precise ? G::ALL : G::DIAGONAL;
+  __half *x0, *x1, *pp, *bb, *tt;
+  const int64_t next = up(sh.batch * 2 * np, 128);   // from one square matrix to the next
+  double* partial;
   auto layout = [&](Arena& ar) {
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
-    x0 = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * nx));
-    x1 = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * nx));
-    for (Square* q : {&pp, &bb, &tt}) {
-      if (q == &tt && !pairing) continue;
-      q->at = ar.take<__half>((size_t)(sh.batch * G::planes(PL) * np));
-      if (PL != G::ONE_EXACT) continue;
-      q->diff = ar.take<float>((size_t)(sh.batch * ld_p));
-      q->quot = ar.take<float>((size_t)(sh.batch * ld_p));
-    }
+    for (__half** x : {&x0, &x1}) *x = ar.take<__half>((size_t)(sh.batch * 2 * nx));
+    pp = ar.take<__half>((size_t)((pairing ? 3 : 2) * next));
+    bb = pp + next;
+    tt = bb + next;   // where steps are paired
   };
   Arena sizing;
   layout(sizing);
@@ -428,9 +437,17 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   u.partial = partial;
   u.x = x0;
   u.ld_x = ld_x;
-  u.batch_x = G::planes(PL) * nx;
+  u.batch_x = 2 * nx;
   u.plane_x = nx;
-  u.planes = G::planes(PL);
+  u.planes = both[0] ? 2 : 1;
+  if (!precise) {
+    u.squares = pp + np;
+    u.ld_s = ld_p;
+    u.batch_s = 2 * np;
+    u.next_s = next;
+    u.side = (int)m;
+    u.count = pairing ? 3 : 2;
+  }
   u.rows = (int)sh.rows;
   u.cols = (int)sh.cols;
   u.scale = G::kIterScale;
@@ -443,74 +460,67 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   G::Params p{};
   p.rows = p.cols = (int)m;
   p.batch = (int)sh.batch;
+  p.planes = 2;
   p.ld_out = p.ld_x = ld_p;
-  p.batch_out = p.batch_x = G::planes(PL) * np;
+  p.batch_out = p.batch_x = 2 * np;
   p.plane_out = p.plane_x = np;
-  p.ld_dev = ld_p;
-  const auto square = [&](const Square& q) { return Operand{q.at, m, m, ld_p, sh.batch * G::planes(PL), np}; };
-  const auto into = [&](const Square& out, int64_t k) {
-    p.k = (int)k;
-    p.out = out.at;
-    p.diff_out = out.diff;
-    p.quot_out = out.quot;
-    p.dev_r = p.dev_c = nullptr;
-  };
+  p.second_out = squares;
+  const auto square = [&](const __half* q) { return Operand{q, m, m, ld_p, sh.batch * 2, np}; };
   // out = B(x) with the coefficients of step s; out = x y
-  const auto polynomial = [&](const Square& out, const Square& x, int s) {
-    into(out, m);
-    p.x = x.at;
-    p.dev_r = p.dev_c = x.diff;
-    p.fa = flat[3 * s];
-    p.fb = flat[3 * s + 1];
-    p.fc = flat[3 * s + 2];
-    return run_sym<G::POLY, false, PL>(square(x), square(x), p, nsm, st);
+  const auto polynomial = [&](__half* out, const __half* x, int s) {
+    G::Params q = p;
+    q.k = (int)m;
+    q.second_r = q.second_c = squares;
+    q.out = out;
+    q.x = x;
+    q.fa = flat[3 * s];
+    q.fb = flat[3 * s + 1];
+    q.fc = flat[3 * s + 2];
+    return run_sym<G::POLY, false>(square(x), square(x), q, nsm, st);
   };
-  const auto product = [&](const Square& out, const Square& x, const Square& y) {
-    into(out, m);
-    p.dev_r = x.quot;
-    p.dev_c = y.quot;
-    return run_sym<G::GRAM, false, PL>(square(x), square(y), p, nsm, st);
+  const auto product = [&](__half* out, const __half* x, const __half* y) {
+    G::Params q = p;
+    q.k = (int)m;
+    q.second_r = q.second_c = squares;
+    q.out = out;
+    return run_sym<G::GRAM, false>(square(x), square(y), q, nsm, st);
   };
   for (int s = 0; s < steps && rc == BCJR_OK;) {
-    // pairs of steps from the front, one alone before the last three if their number is odd; their product has to
-    // stay within fp16's headroom
-    const int left = steps - s;
-    const bool two = pairing && (left >= 4 || left == 2) && reach[s] * reach[s + 1] <= 15.f;
+    const bool two = pairing && s == 0 && reach[0] * reach[1] <= 15.f;   // their product stays within fp16's headroom
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
-    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * G::planes(PL), nx};
-    into(pp, tall ? sh.rows : sh.cols);
-    rc = tall ? run_sym<G::GRAM, true, PL>(x, x, p, nsm, st) : run_sym<G::GRAM, false, PL>(x, x, p, nsm, st);
+    const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * 2, nx};
+    G::Params gram = p;
+    gram.k = (int)(tall ? sh.rows : sh.cols);
+    gram.second_r = gram.second_c = precise ? G::ALL : G::NONE;
+    gram.out = pp;
+    rc = tall ? run_sym<G::GRAM, true>(x, x, gram, nsm, st) : run_sym<G::GRAM, false>(x, x, gram, nsm, st);
     if (rc || (rc = polynomial(bb, pp, s))) break;
     if (two && ((rc = product(tt, bb, pp)) || (rc = product(pp, tt, bb)) || (rc = polynomial(tt, pp, s + 1)) ||
                 (rc = product(pp, tt, bb))))
       break;
+    const G::Second second = both[s] ? G::ALL : G::NONE;
     s += two ? 2 : 1;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
-    const Square& b = two ? pp : bb;
-    const Operand poly = square(b);
+    const Operand poly = square(two ? pp : bb);
     const bool end = s == steps;
     G::Params q = end ? last : G::Params{};
     q.rows = (int)sh.cols;
     q.cols = (int)sh.rows;
     q.k = (int)m;
     q.batch = (int)sh.batch;
-    q.ld_dev = ld_p;
-    (tall ? q.dev_r : q.dev_c) = b.quot;
+    q.planes = 2;
+    (tall ? q.second_r : q.second_c) = squares;
+    (tall ? q.second_c : q.second_r) = second;
     if (!end) {
       q.out = x1;
       q.ld_out = ld_x;
-      q.batch_out = G::planes(PL) * nx;
+      q.batch_out = 2 * nx;
       q.plane_out = nx;
+      q.second_out = both[s] ? G::ALL : G::NONE;
     }
-#define BCJR_ITER(E) (tall ? run_iter<E, false, PL>(poly, x, q, nsm, st) : run_iter<E, true, PL>(x, poly, q, nsm, st))
-    if (!end) {
-      rc = BCJR_ITER(G::ITER);
-    } else if constexpr (PL == G::ONE) {
-      rc = epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
-    } else {
-      rc = BCJR_ITER(G::LAST);
-    }
+#define BCJR_ITER(E) (tall ? run_iter<E, false>(poly, x, q, nsm, st) : run_iter<E, true>(x, poly, q, nsm, st))
+    rc = !end ? BCJR_ITER(G::ITER) : epi == G::STEP ? BCJR_ITER(G::STEP) : BCJR_ITER(G::LAST);
 #undef BCJR_ITER
     std::swap(x0, x1);
   }
@@ -647,15 +657,7 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
   G::Params last{};
   last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // One plane of 11 bits leaves an error of about 1e-3, less than bf16's own rounding (1.7e-3); fp16 shows more.
-  // Diagonals are nearly constant (gemm::finish) for shorter sides of up to 64, and of up to 256 in long matrices: a bf16
-  // result's error is 1.1 to 1.2 times that of rounding the exact result with them kept, up to 1.7 without (160 x 6788);
-  // of other shapes at most 1.35 without, where it would cost up to 11 % (16 x 333 x 130: 95 us without, 106 with).
-  const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
-#define BCJR_NS(PL) run_newton_schulz<PL>(sh, u, g_type, steps, coeffs, G::LAST, last, st)
-  if (out_type != BCJR_BF16) return BCJR_NS(G::TWO);
-  return m <= 64 || (m <= 256 && n >= 4 * m) ? BCJR_NS(G::ONE_EXACT) : BCJR_NS(G::ONE);
-#undef BCJR_NS
+  return run_newton_schulz(sh, u, g_type, steps, coeffs, G::LAST, out_type != BCJR_BF16, last, st);
 }
 
 int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad, float* momentum,
@@ -676,7 +678,7 @@ int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int6
   last.out = w; last.ld_out = ld_w;
   last.keep = (float)(1.0 - (double)lr * (double)weight_decay);
   last.rate = (float)((double)lr * (double)scale);
-  return run_newton_schulz<G::ONE>(sh, u, grad_type, steps, coeffs, G::STEP, last, static_cast<cudaStream_t>(stream));
+  return run_newton_schulz(sh, u, grad_type, steps, coeffs, G::STEP, false, last, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -48,20 +48,31 @@ enum Epilogue {
 };
 enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 
-// The iterates are kept as fp16(2^12 x), or for outputs of more than 8 bits as the
-// sum of two such planes (the value and what its rounding left: 22 bits), whose
-// product takes three passes over k: R0 C0 + R0 C1 + R1 C0.  With 2^12, |x| <= 16
-// stays finite, and values are rounded to 11 bits down to 2^-26 instead of 2^-14
-// (the entries of a large matrix of norm 1 are that small).
+// Iterates and the square matrices are kept as fp16(2^12 x), one plane of 11 bits, and
+// what its rounding left as a second one (22 bits in all).  With 2^12, |x| <= 16 stays
+// finite, and values are rounded to 11 bits down to 2^-26 instead of 2^-14 (the entries
+// of a large matrix of norm 1 are that small).
+//
+// Which second planes a product needs for a result of 8 bits:
+//   X in B X: all of it.  A rounding E of X is added to X, puts a share of |E| into
+//     directions where X has next to nothing, and every step multiplies those by up to
+//     a = 3.4445 (485 times in five).  With one plane a result of rank 1 is off by 15 %,
+//     of rank 8 by 4 %.
+//   X in X X^T: none.  It would change P by less than P's own rounding.
+//   P and B: the diagonal.  Roundings of B multiply X, so their errors stay in proportion
+//     to each direction and average out over a row, as do those of P, which only enters B.
+//     Not so a diagonal's: P and B may be nearly constant there (then their roundings all
+//     go one way), and a I next to a product that nearly cancels it makes an error of half
+//     a step of a (rank 1, 1536 x 6145, two steps at once: 1 %).  Of the second
+//     planes' blocks of 256 on the diagonal, zeros but for it, a product takes those of
+//     its tile's own rows: one to four blocks of k more.
+// So held, a result is within 1.3e-3 of the exact iteration in the 2-norm whatever its
+// singular values (1.8e-3 at 7 x 9; half of that for updates of full rank).  For results of more than 8 bits
+// every product takes all second planes: R0 C0 + R0 C1 + R1 C0.
 constexpr float kIterScale = 4096.f;
 
-// How iterates and Gram matrices are held (PL below).
-enum Planes {
-  ONE = 1,         // one plane
-  TWO = 2,         // two
-  ONE_EXACT = 3    // one, and what rounding took from the diagonals of the symmetric matrices (see finish)
-};
-__host__ __device__ constexpr int planes(int pl) { return pl == TWO ? 2 : 1; }
+// Which part of an operand's or a result's second plane counts.
+enum Second { NONE = 0, DIAGONAL = 1, ALL = 2 };
 
 struct Params {
   int rows, cols, k;         // extents of r, c, k
@@ -69,6 +80,8 @@ struct Params {
   int tiles;                 // tiles of one matrix
   int batch;
   int splits;                // blocks of one tile (the cluster of tile_kernel)
+  int second_r, second_c;    // Second, of the operands
+  int planes;                // of the operands of one matrix of the batch, one after the other in their maps' third dimension
   int band;                  // pair_kernel: tiles along r of a band
   // MX
   const uint8_t* sr;         // scales of R: sr[(r >> shift_r) * ld_sr + k / 128]
@@ -79,14 +92,10 @@ struct Params {
   // epilogue
   void* out;
   const __half* x;           // P (POLY), laid out as D
-  // ONE_EXACT: what rounding took from the diagonals of the operands along r and along c, or null (POLY: the
-  // differences; else the quotients), and from that of the result.
-  const float *dev_r, *dev_c;
-  float *diff_out, *quot_out;
-  int64_t ld_dev;            // from one matrix of the batch to the next
   int64_t ld_out, ld_x;
   int64_t batch_out, batch_x;
-  int64_t plane_out, plane_x;   // TWO: from one plane to the other
+  int64_t plane_out, plane_x;   // from one plane to the other
+  int second_out;               // Second, of the result and of x
   int out_type;
   float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
@@ -110,121 +119,103 @@ __device__ __forceinline__ void store_columns(void* out, int64_t at, int64_t ld,
   }
 }
 
-// What the end of W columns of a row reads, loaded ahead: W entries of row r of P
-// (symmetric, so they lie side by side; ld_x is a multiple of 8).
-template <int W, int PL>
-struct Ahead {
-  uint4 h[planes(PL)][W / 8];
-  float4 dev[PL == ONE_EXACT ? W / 4 : 1];   // of the columns
-};
-template <int EPI, int W, int PL>
-__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W, PL>& a) {
-  if (EPI == POLY && r < p.rows) {
-    const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x + c0;
-#pragma unroll
-    for (int l = 0; l < planes(PL); ++l)
-#pragma unroll
-      for (int i = 0; i < W / 8; ++i)
-        a.h[l][i] = c0 + 8 * i < p.cols ? __ldcg(reinterpret_cast<const uint4*>(x + l * p.plane_x + 8 * i)) : make_uint4(0, 0, 0, 0);
-  }
-  if (PL == ONE_EXACT && p.dev_c != nullptr) {
-    const float* d = p.dev_c + batch * p.ld_dev + c0;
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i)
-      a.dev[PL == ONE_EXACT ? i : 0] = c0 + 4 * i < p.cols ? __ldcg(reinterpret_cast<const float4*>(d + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+// Whether the diagonal passes through columns c0..c0+W-1 of the warp's rows.
+template <int W>
+__device__ __forceinline__ bool on_diagonal(int r, int c0) {
+  return c0 < (r & ~31) + 32 && c0 + W > (r & ~31);
 }
-// The row's own deviation.
-template <int EPI, int PL>
-__device__ __forceinline__ float row_deviation(const Params& p, int64_t batch, int r) {
-  if (PL != ONE_EXACT || p.dev_r == nullptr || r >= p.rows) return EPI == POLY ? 0.f : 1.f;
-  return __ldcg(p.dev_r + batch * p.ld_dev + r);
+
+// What the end of W columns of a row reads, loaded ahead: W entries of row r of P
+// (symmetric, so they lie side by side; ld_x is a multiple of 8), and what rounding took
+// from all of them or from the diagonal's.
+template <int W>
+struct Ahead {
+  uint4 h[W / 8], l[W / 8];
+  __half diagonal;
+};
+template <int EPI, int W>
+__device__ __forceinline__ void load_ahead(const Params& p, int64_t batch, int r, int c0, Ahead<W>& a) {
+  if (EPI == POLY && r < p.rows) {
+    const __half* x = p.x + batch * p.batch_x + (int64_t)r * p.ld_x;
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+      const bool in = c0 + 8 * i < p.cols;
+      a.h[i] = in ? __ldcg(reinterpret_cast<const uint4*>(x + c0 + 8 * i)) : make_uint4(0, 0, 0, 0);
+      a.l[i] = in && p.second_out == ALL ? __ldcg(reinterpret_cast<const uint4*>(x + p.plane_x + c0 + 8 * i)) : make_uint4(0, 0, 0, 0);
+    }
+    a.diagonal = p.second_out != ALL && on_diagonal<W>(r, c0) ? __ldcg(x + p.plane_x + r) : __float2half_rn(0.f);
+  }
 }
 
 // Stores columns c0..c0+W-1 (as far as they exist) of row r.
-//
-// The diagonals of the symmetric matrices of a small or long X are nearly constant, so their roundings to 11 bits all
-// go the same way, and a few steps of that are an error of 2.4e-3 (160 x 6788) where independent roundings leave
-// 0.8e-3.  With ONE_EXACT what rounding took from a diagonal is therefore kept in fp32: as a difference d, with which
-// P^2 is (P16^2)_rc + P_rc (d_r + d_c) to first order, and as a quotient, by which the rows and columns of the other
-// products are multiplied (right for the diagonal's part of the sum, and nothing next to the rest's own rounding).
-template <int EPI, int W, int PL>
-__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, float dev_row,
-                                       const Ahead<W, PL>& a, float (&v)[W]) {
-  if (r >= p.rows) return;
+template <int EPI, int W>
+__device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, int c0, bool mirror, const Ahead<W>& a,
+                                       float (&v)[W]) {
+  constexpr bool SQUARE = EPI == GRAM || EPI == POLY;
+  if (!SQUARE && EPI != ITER && r >= p.rows) return;   // (the others' lanes exchange values below)
   const int n = p.cols - c0;
   const int64_t at = batch * p.batch_out + (int64_t)c0 * p.ld_out + r;
   const float unit = EPI == OUT ? p.fa : EPI == LAST ? 1.f / (kIterScale * kIterScale) : 1.f / kIterScale;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] *= unit;
-  if constexpr (PL == ONE_EXACT && EPI != POLY) {
-    if (p.dev_c != nullptr) {
-      const float* d = reinterpret_cast<const float*>(a.dev);
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] *= dev_row * d[i];
-    } else if (p.dev_r != nullptr) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] *= dev_row;
-    }
-  }
   if constexpr (EPI == OUT || EPI == LAST) {
     if (p.out_type == OUT_F32) store_columns<OUT_F32, W>(p.out, at, p.ld_out, n, v);
     else if (p.out_type == OUT_F16) store_columns<OUT_F16, W>(p.out, at, p.ld_out, n, v);
     else store_columns<OUT_BF16, W>(p.out, at, p.ld_out, n, v);
-  } else if constexpr (EPI == GRAM || EPI == POLY || EPI == ITER) {
-    const int warp_row = r & ~31;
-    const bool diagonal = c0 < warp_row + 32 && c0 + W > warp_row;   // it passes through the warp's rows
+  } else if constexpr (SQUARE || EPI == ITER) {
+    const bool diagonal = SQUARE && on_diagonal<W>(r, c0);
     if constexpr (EPI == POLY) {
-      const __half* x = reinterpret_cast<const __half*>(a.h);   // W values, then what they left
-      const float* d = reinterpret_cast<const float*>(a.dev);
-      const float on_diagonal = fmaf(p.fa, kIterScale, PL == ONE_EXACT ? p.fb * dev_row : 0.f);
+      const __half *x = reinterpret_cast<const __half*>(a.h), *l = reinterpret_cast<const __half*>(a.l);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float pv = PL == TWO ? __half2float(x[i]) + __half2float(x[(planes(PL) - 1) * W + i]) : __half2float(x[i]);
-        if (PL == ONE_EXACT) v[i] = fmaf(pv * (1.f / kIterScale), dev_row + d[i], v[i]);
-        v[i] = fmaf(p.fb, pv, p.fc * v[i]);
-      }
+      for (int i = 0; i < W; ++i) v[i] = fmaf(p.fb, __half2float(x[i]) + __half2float(l[i]), p.fc * v[i]);
       if (diagonal) {
+        const float add = fmaf(p.fa, kIterScale, p.fb * __half2float(a.diagonal));
+        // (as a sum of products with 0 and 1: a selection becomes an index into local memory)
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = fmaf(i == r - c0 ? 1.f : 0.f, on_diagonal, v[i]);
+        for (int i = 0; i < W; ++i) v[i] = fmaf(i == r - c0 ? 1.f : 0.f, add, v[i]);
       }
     }
-    // (as a sum of products with 0 and 1: a selection becomes an index into local memory)
-    float exact = 0.f;
-    const bool keep = PL == ONE_EXACT && EPI != ITER && diagonal;
-    if (keep) {
+    alignas(16) __half h[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) h[i] = __float2half_rn(v[i]);
+    __half* out = static_cast<__half*>(p.out) + batch * p.batch_out;
+    // the row's own values, side by side: 16-byte aligned; whole groups of 8 stay inside the row's room (ld_out is the
+    // columns rounded up to 8)
+    auto reflect = [&](const __half(&u)[W], __half* to) {
+      if (SQUARE && mirror && r < p.rows) {
+#pragma unroll
+        for (int j = 0; j < W / 8; ++j)
+          if (8 * j < n) reinterpret_cast<uint4*>(to + (int64_t)r * p.ld_out + c0)[j] = reinterpret_cast<const uint4*>(u)[j];
+      }
+    };
+    reflect(h, out);
+    if (p.second_out == ALL) {
+      // Neighbouring lanes exchange halves: the even one stores both lanes' values, the odd one both lanes' second
+      // planes, 4 bytes each, so two planes take as many stores as one (behind an odd number of rows there is room).
+      alignas(16) __half l[W];
+      const bool odd = r & 1;
+      uint32_t* to = reinterpret_cast<uint32_t*>(out + (odd ? p.plane_out : 0) + (int64_t)c0 * p.ld_out + (r & ~1));
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        v[i] = i < n ? v[i] : 0.f;     // columns that do not exist hold anything, NaN too
-        exact = fmaf(i == r - c0 ? 1.f : 0.f, v[i], exact);
+        l[i] = __float2half_rn(v[i] - __half2float(h[i]));
+        const uint32_t own = (uint32_t)__half_as_ushort(h[i]) | ((uint32_t)__half_as_ushort(l[i]) << 16);
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+        if (i < n && (r & ~1) < p.rows) *to = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+        to += p.ld_out / 2;
       }
-    }
-#pragma unroll
-    for (int plane = 0; plane < planes(PL); ++plane) {
-      alignas(16) __half h[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        h[i] = __float2half_rn(v[i]);
-        if (PL == TWO) v[i] -= __half2float(h[i]);
-      }
-      if (keep && (unsigned)(r - c0) < (unsigned)W) {
-        const float back = __half2float(__float2half_rn(exact));
-        p.diff_out[batch * p.ld_dev + r] = exact - back;
-        p.quot_out[batch * p.ld_dev + r] = back != 0.f ? __fdividef(exact, back) : 1.f;   // 1 to within 2^-11: full precision is not needed
-      }
-      __half* to = static_cast<__half*>(p.out) + at + plane * p.plane_out;
+      reflect(l, out + p.plane_out);
+    } else if (r < p.rows) {
+      __half* to = out + (int64_t)c0 * p.ld_out + r;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         if (i < n) *to = h[i];
         to += p.ld_out;
       }
-      if (EPI != ITER && mirror) {
-        // the row's own values, side by side: 16-byte aligned; whole groups of 8 stay inside the row's room
-        // (ld_out is the columns rounded up to 8)
-        __half* m = static_cast<__half*>(p.out) + batch * p.batch_out + plane * p.plane_out + (int64_t)r * p.ld_out + c0;
+      if (diagonal && (unsigned)(r - c0) < (unsigned)min(W, n)) {
+        float left = 0.f;
 #pragma unroll
-        for (int j = 0; j < W / 8; ++j)
-          if (8 * j < n) reinterpret_cast<uint4*>(m)[j] = reinterpret_cast<const uint4*>(h)[j];
+        for (int i = 0; i < W; ++i) left = i == r - c0 ? v[i] - __half2float(h[i]) : left;
+        out[p.plane_out + (int64_t)r * p.ld_out + r] = __float2half_rn(left);
       }
     }
   } else {   // STEP
@@ -270,15 +261,44 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, int64_t ld, int s
   return w;
 }
 
-// Place of block kb of k: operands of two planes are gone through three times.  The
-// first value of k, the third coordinates of R and C in their maps.
-template <int KIND, int PL>
-__device__ __forceinline__ void block_place(int kb, int blocks, int batch, int* k, int* zr, int* zc) {
-  const int pass = PL != TWO || kb < blocks ? 0 : kb < 2 * blocks ? 1 : 2;
-  *k = (kb - pass * blocks) * (KIND == MX ? 128 : 64);
-  *zr = batch * planes(PL) + (pass == 2 ? 1 : 0);
-  *zc = batch * planes(PL) + (pass == 1 ? 1 : 0);
-}
+// The blocks of k of a tile at row r0 and column c0 (of the pair's whole tile): all of k; then again, for what counts of
+// C's second plane; then of R's.  On the diagonal, that is where k is one of the tile's own columns or rows.
+template <int KIND, int TR, int TC>
+struct Blocks {
+  int all, first_c, in_c, first_r, in_r;
+  __device__ __forceinline__ Blocks(const Params& p, int blocks, int r0, int c0) : all(blocks), first_c(0), in_c(0), first_r(0), in_r(0) {
+    if (KIND == MX) return;
+    if (p.second_c == DIAGONAL) {
+      first_c = c0 / 64;
+      in_c = min(TC / 64, blocks - first_c);
+    } else if (p.second_c == ALL) {
+      in_c = blocks;
+    }
+    if (p.second_r == DIAGONAL) {
+      first_r = r0 / 64;
+      in_r = min(TR / 64, blocks - first_r);
+    } else if (p.second_r == ALL) {
+      in_r = blocks;
+    }
+  }
+  __device__ __forceinline__ int total() const { return all + in_c + in_r; }
+  // The first value of k of block kb, the third coordinates of R and C in their maps.
+  __device__ __forceinline__ void place(const Params& p, int kb, int batch, int* k, int* zr, int* zc) const {
+    *zr = *zc = batch * p.planes;
+    int b = kb;
+    if (KIND == F16 && kb >= all) {
+      b = kb - all;
+      if (b < in_c) {
+        b += first_c;
+        ++*zc;
+      } else {
+        b += first_r - in_c;
+        ++*zr;
+      }
+    }
+    *k = b * (KIND == MX ? 128 : 64);
+  }
+};
 
 // Tile t of a symmetric product of TR-row and TC-column tiles: row tile j has the
 // (j + 1) TR / TC column tiles up to its diagonal block.
@@ -336,7 +356,7 @@ struct TileShape {
 // is latency, not a pipe: of the 6 us of a product of 512 x 512 x 2048 the first
 // copy takes 0.8, eight stages 1.7 (64 bytes a clock and SM from L2), the exchange
 // 2.0, the stores 0.9.  One token through 8192 x 2048 (17 MB): 6.5 us, 2.6 TB/s.
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
                                                              const __grid_constant__ CUtensorMap map_c, const Params p) {
   using S = TileShape<KIND, BN>;
@@ -369,7 +389,8 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   }
   const int r0 = tr * kRowsTile, c0 = tcn * BN;
   const int blocks = (p.k + kElems - 1) / kElems;
-  const int total = PL == TWO ? 3 * blocks : blocks;
+  const Blocks<KIND, kRowsTile, BN> order(p, blocks, r0, c0);
+  const int total = order.total();
   const int kb0 = (int)((int64_t)total * rank / p.splits), kb1 = (int)((int64_t)total * (rank + 1) / p.splits);
 
   if (threadIdx.x == 0) {
@@ -401,8 +422,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   // the columns whose sums this warp finishes: units of eight, one in 4 * splits
   const int row = r0 + 32 * (warp & 3) + lane;
   const int unit0 = rank + p.splits * ((warp - 2) >> 2), step = 4 * p.splits;
-  Ahead<8, PL> ahead;
-  float dev_row = 1.f;
+  Ahead<8> ahead;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -416,7 +436,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         const uint32_t dst = ring + s * S::kStageBytes, bar = full + 8 * s;
         tc::mbar_expect(bar, S::kStageBytes);
         int k, zr, zc;
-        block_place<KIND, PL>(kb, blocks, batch, &k, &zr, &zc);
+        order.place(p, kb, batch, &k, &zr, &zc);
         if (R_MN) {
           tc::tma_load3(dst, &map_r, r0, k, zr, bar);
           tc::tma_load3(dst + 8192, &map_r, r0 + 64, k, zr, bar);
@@ -491,8 +511,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
         tc::mbar_arrive(sfull + 8 * ss);
       }
     }
-    if (unit0 < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c0 + 8 * unit0, ahead);
-    dev_row = row_deviation<EPI, PL>(p, batch, row);
+    if (unit0 < kUnits) load_ahead<EPI, 8>(p, batch, row, c0 + 8 * unit0, ahead);
     ok = ok && tc::mbar_wait(done, 0);
     if (!ok) gave_up();
   }
@@ -551,9 +570,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
           v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
         }
       }
-      const Ahead<8, PL> now = ahead;
-      if (u + step < kUnits) load_ahead<EPI, 8, PL>(p, batch, row, c + 8 * step, ahead);
-      finish<EPI, 8, PL>(p, batch, row, c, mirror, dev_row, now, v);
+      const Ahead<8> now = ahead;
+      if (u + step < kUnits) load_ahead<EPI, 8>(p, batch, row, c + 8 * step, ahead);
+      finish<EPI, 8>(p, batch, row, c, mirror, now, v);
     }
   }
   tc::fence_before();
@@ -599,7 +618,7 @@ struct PairShape {
 // bounds it is the SMs' way to L2 (60 KB a stage and block at 64 bytes a clock, about
 // as long as the products) with the stores on the same way (without them 106 us).
 // fp16 256 x 256 tiles: 0.29 us for 64 values of k, the tensor cores' own rate 0.27.
-template <int KIND, int BN, bool R_MN, bool C_MN, int EPI, int PL>
+template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ CUtensorMap map_r,
                                                                 const __grid_constant__ CUtensorMap map_c, const Params p) {
   using S = PairShape<KIND, BN>;
@@ -624,7 +643,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int all = p.tiles * p.batch;
   const int blocks = (p.k + kElems - 1) / kElems;   // > 0
-  const int total = PL == TWO ? 3 * blocks : blocks;
+  using Order = Blocks<KIND, 2 * kRowsTile, BN>;
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_r);
@@ -680,6 +699,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         bool mirror;
         place(tile, &r0, &c0, &batch, &mirror);
         const int ch = c0 + (int)rank * kHalf;
+        const Order order(p, blocks, r0 - (int)rank * kRowsTile, c0);
+        const int total = order.total();
         for (int kb = 0; kb < total; kb += S::kSub, ++it) {
           const int s = it % S::kStages, n = min(S::kSub, total - kb);
           ok = tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
@@ -689,7 +710,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
           for (int j = 0; j < n; ++j) {
             const uint32_t dst = ring + s * S::kStageBytes + j * S::kSubBytes;
             int k, zr, zc;
-            block_place<KIND, PL>(kb + j, blocks, batch, &k, &zr, &zc);
+            order.place(p, kb + j, batch, &k, &zr, &zc);
             if (R_MN) {
               tc::tma_load3_pair(dst, &map_r, r0, k, zr, bar);
               tc::tma_load3_pair(dst + 8192, &map_r, r0 + 64, k, zr, bar);
@@ -725,6 +746,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = acc + set * BN;
+        int r0, c0, batch;
+        bool mirror;
+        place(tile, &r0, &c0, &batch, &mirror);
+        const int total = Order(p, blocks, r0, c0).total();
         for (int kb = 0; kb < total; kb += S::kSub, ++it) {
           const int s = it % S::kStages;
           ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1));
@@ -833,10 +858,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       bool mirror;
       place(tile, &r0, &c0, &batch, &mirror);
       const int set = n % S::kSets, row = r0 + 32 * (warp & 3) + lane;
-      Ahead<16, PL> ahead;
+      Ahead<16> ahead;
       uint32_t u[16];
-      load_ahead<EPI, 16, PL>(p, batch, row, c0 + 16 * first, ahead);
-      const float dev_row = row_deviation<EPI, PL>(p, batch, row);
+      load_ahead<EPI, 16>(p, batch, row, c0 + 16 * first, ahead);
       ok = tc::mbar_wait(accfull + 8 * set, (n / S::kSets) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok && *fail == 0);
       if (!ok) break;
@@ -849,12 +873,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         float v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
-        const Ahead<16, PL> now = ahead;
+        const Ahead<16> now = ahead;
         if (c + 32 < BN) {
           tc::tmem_ld16(sums + set * BN + c + 32, u);
-          load_ahead<EPI, 16, PL>(p, batch, row, c0 + c + 32, ahead);
+          load_ahead<EPI, 16>(p, batch, row, c0 + c + 32, ahead);
         }
-        finish<EPI, 16, PL>(p, batch, row, c0 + c, mirror, dev_row, now, v);
+        finish<EPI, 16>(p, batch, row, c0 + c, mirror, now, v);
       }
       tc::tmem_drain_ld();
       tc::fence_before();

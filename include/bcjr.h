@@ -265,11 +265,15 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * X_0 = G / (||G||_F + eps) and, for each of `steps` steps and its coefficients
  * (a, b, c), X <- a X + (b A + c A^2) X where A = X X^T (X^T X from the right
  * when rows > cols), out is the last X: G with its singular values moved
- * towards 1.  Products sum in fp32.  For a bf16 out their operands, the iterates
- * and Gram matrices, are fp16 scaled by 2^12 (11 bits), which keeps out within
- * about 1e-3 of the exact iteration in the 2-norm, less than its own rounding;
- * for an fp16 out they are pairs of such values (22 bits, three times the
- * products), and out is within about 2e-5 before it is rounded.
+ * towards 1.  Products sum in fp32.  Their operands, the iterates and Gram
+ * matrices, are fp16 scaled by 2^12 (11 bits) and, where it counts, what that
+ * rounding left as a second such value (22 bits).  For a bf16 out these are the
+ * iterates that are multiplied (but the last, which 11 bits hold well enough) and
+ * the diagonals, which keeps out within about 1e-3 of the exact iteration in the
+ * 2-norm (2e-3 at most), less than its own rounding, whatever the singular values
+ * of G; for an fp16 out all of them (three times the products), which leaves 1e-4
+ * before it is rounded, or where few directions carry G what the fp32 sums leave
+ * in the others and the steps amplify: 2e-4 (512 x 512) to 1.1e-3 (2048 x 2048).
  *   g       [batch][rows][cols]  fp32, fp16 or bf16 (input)
  *   coeffs  [steps][3]           HOST pointer, read during the call, or NULL
  *                                for Muon's (3.4445, -4.7750, 2.0315)
@@ -277,10 +281,10 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * batch <= 32767, rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.  Coefficients that drive a
  * singular value of [0, 1] above 2 are BCJR_ERR_INVALID_ARG.  A matrix of zeros
  * gives zeros (eps > 0); NaN or infinities make that matrix NaN.  Entries of X_0
- * below 2^-36 vanish (so does a G whose norm is that far below eps).  Directions
- * whose singular values are small against ||G||_F are amplified (Muon's default: up
- * to 485 times), rounding with them: where only those carry the result, as with a
- * matrix of few strong directions, the error of a bf16 out grows to some percent.
+ * below 2^-36 vanish (so does a G whose norm is that far below eps).  Steps amplify
+ * the directions whose singular values are small against ||G||_F (Muon's default:
+ * up to 485 times), what G itself holds there, such as the rounding of a bf16 G,
+ * included.
  */
 BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g,
                                 int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out,
@@ -293,7 +297,8 @@ BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_
  *   w        <- (1 - lr weight_decay) w - lr scale orthogonalise(u)
  *   w, momentum  [rows][cols] fp32 (updated), grad [rows][cols] fp32, fp16 or bf16
  * steps, coeffs and eps as in bcjr_orthogonalise, operands as for its bf16
- * output; lr, mu, weight_decay and scale finite.
+ * output (the orthogonalised update is as near as that before it is rounded); lr, mu,
+ * weight_decay and scale finite.
  */
 BCJR_API int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad,
                             float* momentum, int64_t ld_momentum, int64_t rows, int64_t cols, float lr, float mu,

@@ -1,0 +1,116 @@
+"""How near the orthogonalisation and the Muon step come to their 64-bit forms, on
+updates of every kind: few directions, many, nearly orthogonal, thin, long, and the
+sizes of whole layers."""
+import math
+
+import pytest
+import torch
+
+import layer_reference as ref
+from bcjr_sum_product_b200 import lib
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HALF_STEP = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+def randn(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV)
+
+
+def low_rank(rows, cols, rank, seed):
+    return randn(rows, rank, seed=seed) @ randn(rank, cols, seed=seed + 1)
+
+
+def finished():
+    torch.cuda.synchronize()
+    assert lib.get_device_error() == 0
+
+
+def relative(got, want):
+    err = torch.linalg.vector_norm(got.double() - want, dim=(-2, -1)) / torch.linalg.vector_norm(want, dim=(-2, -1))
+    return float(err.max())
+
+
+def orthogonal_part(u, **kw):
+    """What muon_step adds to weights of zero, from momentum zero without nesterov: -orthogonalise(u) in fp32."""
+    w = torch.zeros(u.shape, device=DEV)
+    lib.muon_step(w, u, torch.zeros(u.shape, device=DEV), 1.0, mu=0.0, nesterov=False, scale=1.0, **kw)
+    return -w
+
+
+# ---------------------------------------------------------------- few directions
+
+def bound(steps, paired):
+    """2-norm of the error over that of the result.  P and B are rounded to 11 bits, their diagonals to 22: independent
+    errors of at most 2^-11 / sqrt(3) of each in the 2-norm.  B x changes in proportion to B's; P's enters through
+    b + 2 c t, up to twice the value of a + b t + c t^2 where singular values end up (t from 0.5 to 1.3), so 1 + 4
+    squares a step; the first two steps at once round three products more, each counted like P.  The last step's X, one plane of
+    11 bits, grows at most 3.4445 times (on its own, so the sum); 22 bits at most 485 times."""
+    one = 2.0 ** -11 / math.sqrt(3)
+    squares = 5 * steps + (12 if paired else 0)
+    return math.sqrt(squares) * one + 3.4445 * one + 485 * 2.0 ** -11 * one
+
+
+SHAPES = [(512, 512), (200, 700), (333, 130), (16, 1000), (64, 64), (129, 129), (1100, 900), (1536, 6145), (6200, 1500)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rank", [1, 8, 60, 250])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_updates_of_few_directions(rows, cols, rank, dtype):
+    """A gradient summed over few tokens has few directions; the others hold nothing but
+    roundings, and every step multiplies those by 3.4445.  (A bf16 update has its own roundings in them, which are
+    part of the matrix.)"""
+    g = low_rank(rows, cols, min(rank, rows, cols), seed=rows + cols + rank).to(dtype)
+    want = ref.newton_schulz(g)
+    tol = bound(5, min(rows, cols) >= 1500)
+    out, u = lib.orthogonalise(g), orthogonal_part(g)
+    finished()
+    assert relative(u, want) <= tol
+    assert relative(out, want) <= tol + HALF_STEP[torch.bfloat16] / math.sqrt(3)
+
+
+def test_few_directions_in_a_batch():
+    g = torch.stack([low_rank(130, 333, r, seed=50 + r) for r in (1, 2, 5, 17, 60, 130)])
+    for x in (g, g.mT.contiguous()):
+        out = lib.orthogonalise(x)
+        finished()
+        assert relative(out, ref.newton_schulz(x)) <= bound(5, False) + HALF_STEP[torch.bfloat16] / math.sqrt(3)
+
+
+@pytest.mark.parametrize("coeffs", [(1.875, -1.25, 0.375), [(3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (0.9, 0.05, 0.0), (3.4445, -4.7750, 2.0315)],
+                                    [(0.5, 0.0, 0.0), (3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (1.0, 0.0, 0.0)]])
+def test_few_directions_with_other_coefficients(coeffs):
+    """Steps that amplify less, or nothing, take the second plane of X or leave it in any order."""
+    co = coeffs if isinstance(coeffs, list) else [coeffs] * 4
+    for g in (low_rank(150, 400, 3, seed=70), low_rank(400, 150, 3, seed=71)):
+        u = orthogonal_part(g, steps=4, coeffs=coeffs)
+        finished()
+        # any X whose second plane is left out may grow four times
+        tol = 3 * 4 * 2.0 ** -12 + 4 * 4 * 2.0 ** -11 / math.sqrt(3)
+        assert relative(u, ref.newton_schulz(g, 4, co)) <= tol
+
+
+# ---------------------------------------------------------------- nearly constant diagonals
+
+@pytest.mark.parametrize("rows,cols", [(33, 5000), (160, 6788), (5632, 165), (16, 100), (64, 300), (400, 30000), (20000, 300), (257, 6000),
+                                       (520, 12000), (1, 50), (40, 1)])
+def test_thin_and_long_updates(rows, cols):
+    """Rows that are nearly orthogonal: the diagonals of P and B are nearly constant, and their roundings would go one
+    way.  Weights of fp32 show all of it."""
+    g = randn(rows, cols, seed=rows + cols)
+    want = ref.newton_schulz(g)
+    out, u = lib.orthogonalise(g), orthogonal_part(g)
+    finished()
+    assert relative(u, want) <= bound(5, min(rows, cols) >= 512)
+    assert relative(out, want) <= bound(5, min(rows, cols) >= 512) + HALF_STEP[torch.bfloat16] / math.sqrt(3)
+
+
+@pytest.mark.parametrize("side", [40, 130, 500, 700])
+def test_updates_that_are_orthogonal_already(side):
+    g, _ = torch.linalg.qr(randn(side, side, seed=side).double())
+    g = g.float().contiguous()
+    u = orthogonal_part(g)
+    finished()
+    assert relative(u, ref.newton_schulz(g)) <= bound(5, False)
