@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include <cuda.h>
@@ -129,13 +130,21 @@ int allow_smem(const void* kern, std::atomic<uint64_t>* done, int smem) {
   return BCJR_OK;
 }
 
+// BCJR_DENSE_TEST_NOFILL=1 (tests only): products stop fetching, so that their bounded waits run out and they report
+// BCJR_ERR_TIMEOUT.
+bool test_nofill() {
+  const char* e = std::getenv("BCJR_DENSE_TEST_NOFILL");
+  return e && e[0] == '1';
+}
+
 // Dependent launch: this kernel's set-up may overlap the end of the kernel before it on
 // the stream, where that one allows it (the library's own do); it waits for that one
 // before it touches memory.
 template <class Kern>
 int launch(Kern kern, int64_t grid, int64_t batch, int threads, int smem, int cluster, const CUtensorMap& mr,
-           const CUtensorMap& mc, const G::Params& p, cudaStream_t st) {
+           const CUtensorMap& mc, G::Params p, cudaStream_t st) {
   if (grid > INT32_MAX) return BCJR_ERR_UNSUPPORTED;
+  p.nofill = test_nofill() ? 1 : 0;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;

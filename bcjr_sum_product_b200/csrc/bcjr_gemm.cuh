@@ -99,6 +99,7 @@ struct Params {
   int out_type;
   float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
+  int nofill;                // tests: the last block of a cluster fetches one stage and no more, so that waits run out
 };
 
 constexpr int kRowsTile = 128;                      // rows of a block's tile
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
       int issued = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         const int s = issued % S::kStages;
+        if (p.nofill && rank + 1 == p.splits && issued > 0) break;
         if (!tc::mbar_wait(empty + 8 * s, ((issued / S::kStages) & 1) ^ 1)) {
           gave_up();
           break;
@@ -520,13 +522,15 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
   tc::fence_after();
 
   // The sums: lane r of the warp's quarter, eight columns at a time.
-  const bool usable = *fail == 0, some = kb1 > kb0;
+  const bool some = kb1 > kb0;
   const uint32_t sums = acc + ((uint32_t)(32 * (warp & 3)) << 16);
   const int rl = 32 * (warp & 3) + lane;
   // Unit u is finished by rank u % splits; its sums from rank s lie over the stages of that block (no
   // copy is in flight there after the first cluster barrier) as [u / splits][s][two halves][128 rows] float4.
   if (p.splits > 1) {
     tc::cluster_sync();
+    // the sums of a block that gave up are incomplete: none of the cluster's may be stored
+    if (threadIdx.x < p.splits && *fail != 0) tc::st_cluster(tc::map_rank(slot + 4, threadIdx.x), 1);
     if (warp >= 2) {
 #pragma unroll 2
       for (int u = (warp - 2) >> 2; u < kUnits; u += 4) {
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constan
     }
     tc::cluster_sync();
   }
-  if (warp >= 2 && usable) {
+  if (warp >= 2 && *fail == 0) {
 #pragma unroll 1
     for (int u = unit0; u < kUnits; u += step) {
       const int c = c0 + 8 * u;
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
   const uint32_t scales = ring + S::kStages * S::kStageBytes;
   const uint32_t ctl = scales + S::kScaleStages * S::kScaleBytes;
   const uint32_t full = ctl, empty = full + 8 * S::kStages, sfull = empty + 8 * S::kStages,
-                 accfull = sfull + 8 * S::kScaleStages, accempty = accfull + 16, slot = accempty + 16;
+                 accfull = sfull + 8 * S::kScaleStages, accempty = accfull + 16, ended = accempty + 16, slot = ended + 8;
   volatile uint32_t* slot_p = reinterpret_cast<volatile uint32_t*>(smem + (slot - ring));
   volatile int* fail = reinterpret_cast<volatile int*>(smem + (slot + 4 - ring));
 
@@ -657,6 +661,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       tc::mbar_init(accfull + 8 * i, 1);
       tc::mbar_init(accempty + 8 * i, 16);  // eight warps of each block
     }
+    tc::mbar_init(ended, 1);
     *fail = 0;
     tc::mbar_init_fence();
   }
@@ -703,6 +708,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
         const int total = order.total();
         for (int kb = 0; kb < total; kb += S::kSub, ++it) {
           const int s = it % S::kStages, n = min(S::kSub, total - kb);
+          if (p.nofill && rank == 1 && it > 0) break;
           ok = tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1);
           if (!ok) break;
           const uint32_t bar = tc::map_rank(full + 8 * s, 0);
@@ -790,8 +796,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
       }
       if (!ok) {
         gave_up();
-        if (tc::elect_one()) tc::commit<2>(accfull);      // what was issued ends before the blocks leave (bounded by the readers' wait)
-        tc::mbar_wait(accfull, 0);
+        // what was issued ends before the blocks leave; the tile's sums are incomplete, so both blocks' readers wait in vain
+        if (tc::elect_one()) tc::commit_pair_here(ended);
+        tc::mbar_wait(ended, 0);
       }
     }
   } else if (warp < 4) {

@@ -313,7 +313,8 @@ BCJR_API int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_t
  * VJP for a bulk copy into its shared-memory codeword ring did not end within
  * 1 s, after which that CTA computes on without the ring and its sequences'
  * outputs are not usable; or a wait of a matrix product for its copies or sums,
- * after which that tile is not written).  The flag is one per device and process, shared by
+ * after which that tile, and those that its blocks would have taken next, are not
+ * written: incomplete sums never are).  The flag is one per device and process, shared by
  * all streams; reading it clears it.
  */
 BCJR_API int bcjr_get_device_error(void* stream);

@@ -341,3 +341,41 @@ def test_offsets_past_32_bits():
     finished()
     assert torch.equal(k[-70:, -70:], last)
     assert float(k[:-70, :1000].abs().max()) == 0.0
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("m,n,k", [(20, 256, 8192), (300, 400, 1024), (2048, 2048, 1024), (2048, 4096, 2048)])
+def test_products_whose_waits_run_out_store_nothing(monkeypatch, m, n, k):
+    """With BCJR_DENSE_TEST_NOFILL=1 one block of each cluster fetches a single stage.  The
+    waits for the rest run out after 1 s; no block stores sums that lack it, its peers
+    neither; the next call is right."""
+    x, w = randn(m, k, seed=61).to(DEV), randn(n, k, seed=62).to(DEV)
+    a, b = lib.fp8_quantise(x), lib.fp8_quantise(w, 128)
+    want = lib.fp8_matmul(*a, *b, out_dtype=torch.float32)
+    finished()
+    out = torch.full((m, n), 7.0, device=DEV)
+    monkeypatch.setenv("BCJR_DENSE_TEST_NOFILL", "1")
+    lib.fp8_matmul(*a, *b, out=out)
+    torch.cuda.synchronize()
+    assert lib.get_device_error() == lib.BCJR_ERR_TIMEOUT
+    assert bool((out == 7).all())
+    monkeypatch.delenv("BCJR_DENSE_TEST_NOFILL")
+    assert lib.get_device_error() == 0
+    assert torch.equal(lib.fp8_matmul(*a, *b, out_dtype=torch.float32), want)
+    finished()
+
+
+@pytest.mark.parametrize("rows,cols", [(512, 2048), (2048, 2048)])
+def test_a_muon_step_whose_waits_run_out_leaves_the_weights(monkeypatch, rows, cols):
+    w, g = randn(rows, cols, seed=63).to(DEV), randn(rows, cols, seed=64).to(DEV)
+    before = w.clone()
+    monkeypatch.setenv("BCJR_DENSE_TEST_NOFILL", "1")
+    lib.muon_step(w, g, torch.zeros_like(g), 0.1, steps=1)
+    torch.cuda.synchronize()
+    assert lib.get_device_error() == lib.BCJR_ERR_TIMEOUT
+    assert torch.equal(w, before)
+    monkeypatch.delenv("BCJR_DENSE_TEST_NOFILL")
+    lib.muon_step(w, g, torch.zeros_like(g), 0.1, steps=1)
+    finished()
+    assert not torch.equal(w, before)
