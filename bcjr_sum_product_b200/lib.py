@@ -271,9 +271,32 @@ def _matrix(t: torch.Tensor, name: str, dtypes, ndim: int = 2, device=None) -> t
     return t
 
 
-def _ld(t: torch.Tensor, multiple: int = 1) -> int:
-    """Row stride in elements (for a single row, its length rounded up to `multiple`)."""
-    return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // multiple) * multiple
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements (for a single row, its length)."""
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def _overlap(p: torch.Tensor, q: torch.Tensor) -> bool:
+    """Whether two matrices share memory; rows that lie between the other's rows do not."""
+    (rows_p, cols_p), (rows_q, cols_q) = p.shape, q.shape
+    if not (rows_p and cols_p and rows_q and cols_q):
+        return False
+    at_p, size_p = p.data_ptr(), p.element_size()
+    at_q, size_q = q.data_ptr(), q.element_size()
+    ld_p, ld_q, row_p, row_q = _ld(p) * size_p, _ld(q) * size_q, cols_p * size_p, cols_q * size_q
+    if at_p + (rows_p - 1) * ld_p + row_p <= at_q or at_q + (rows_q - 1) * ld_q + row_q <= at_p:
+        return False
+    # for each row of p the last row of q that starts before its end
+    start_p = at_p + ld_p * torch.arange(rows_p)
+    start_q = at_q + ld_q * torch.arange(rows_q)
+    last = torch.searchsorted(start_q, start_p + row_p) - 1
+    return bool(((last >= 0) & (start_q[last.clamp_min(0)] + row_q > start_p)).any())
+
+
+def _apart(named, out: torch.Tensor, name: str):
+    for other, t in named:
+        if _overlap(out, t):
+            raise ValueError(f"{name} and {other} must not share memory")
 
 
 def _raw_stream(index: int) -> int:
@@ -371,7 +394,8 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
     """bcjr_fp8_matmul: alpha (a scale_a) (b scale_b)^T, [M, N], from 8-bit codes a [M, K]
     and b [N, K] (e4m3 or e5m2 each) with one scale for each 128 values of K and
     each row or 128 rows, as fp8_quantise gives them.  Sums are in fp32, the
-    result (fp32, fp16 or bf16; ``out``, if given, with any row stride) is rounded once."""
+    result (fp32, fp16 or bf16; ``out``, if given, with any row stride and apart from
+    the operands) is rounded once."""
     (M, K), args_a = _scaled(a, scale_a, "a", None)
     device = a.device
     (N, Kb), args_b = _scaled(b, scale_b, "b", device)
@@ -384,6 +408,7 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
         _matrix(out, "out", _WIDE, device=device)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [{M}, {N}]")
+        _apart((("a", a), ("scale_a", scale_a), ("b", b), ("scale_b", scale_b)), out, "out")
     return _call(device, stream, _fp8_matmul, args_a, args_b, M, N, K, alpha, out_dtype, out, device)
 
 
@@ -445,12 +470,14 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: f
     momentum = mu momentum + grad; u = grad + mu momentum (or momentum without
     nesterov); w = (1 - lr weight_decay) w - lr scale orthogonalise(u), the last within
     about 1e-3 in the 2-norm.
-    ``scale`` defaults to sqrt(max(1, rows / cols))."""
+    ``scale`` defaults to sqrt(max(1, rows / cols)).  The three must not share memory."""
     _matrix(w, "w", (torch.float32,))
     _matrix(grad, "grad", _WIDE, device=w.device)
     _matrix(momentum, "momentum", (torch.float32,), device=w.device)
     if grad.shape != w.shape or momentum.shape != w.shape:
         raise ValueError("grad and momentum must have the shape of w")
+    _apart((("momentum", momentum), ("grad", grad)), w, "w")
+    _apart((("grad", grad),), momentum, "momentum")
     rows, cols = w.shape
     if scale is None:
         scale = math.sqrt(max(1.0, rows / cols)) if cols else 1.0

@@ -121,3 +121,23 @@ def test_command_refusals(capsys):
         with pytest.raises(SystemExit):
             qat.main(argv)
     capsys.readouterr()
+
+
+def test_overlap_of_matrices():
+    """Against the sets of bytes: equal and other row strides, types and offsets, rows between rows, single rows."""
+    def bytes_of(t):
+        return {t.data_ptr() + (r * t.stride(0) + c * t.stride(1)) * t.element_size() + i for r in range(t.shape[0])
+                for c in range(t.shape[1]) for i in range(t.element_size())}
+
+    room = torch.zeros(400)
+    half = room.view(torch.float16)
+    views = [room[at:at + 200].as_strided((r, c), (ld, 1), at) for at in (0, 3, 8, 40, 70) for r, c, ld in
+             ((1, 5, 5), (4, 5, 20), (4, 15, 20), (3, 1, 7), (9, 4, 11), (0, 5, 5))]
+    views += [half.as_strided((r, c), (ld, 1), at) for at in (1, 10, 81) for r, c, ld in ((4, 9, 40), (5, 30, 40), (2, 3, 11))]
+    seen = set()
+    for p in views:
+        for q in views:
+            want = bool(bytes_of(p) & bytes_of(q))
+            assert lib._overlap(p, q) == want
+            seen.add(want)
+    assert seen == {True, False}
