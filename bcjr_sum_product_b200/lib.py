@@ -293,6 +293,18 @@ def _overlap(p: torch.Tensor, q: torch.Tensor) -> bool:
     return bool(((last >= 0) & (start_q[last.clamp_min(0)] + row_q > start_p)).any())
 
 
+def _no_gradient(where: str, *tensors):
+    """These operators have no derivative: a result that silently lacks one is refused."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{where} has no derivative: detach its inputs, or call it under torch.no_grad()")
+
+
+def _changed(*tensors):
+    """Tells autograd that the tensors were written."""
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def _apart(named, out: torch.Tensor, name: str):
     for other, t in named:
         if _overlap(out, t):
@@ -342,7 +354,8 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
     ceil(cols / 128)] float8_e8m0fnu); "cols" the same of the transpose of x
     (codes [cols, rows], blocks down the columns of x); "both" all four, from one
     pass over x.  The rows of the codes start at multiples of 16 bytes, as
-    fp8_matmul takes them."""
+    fp8_matmul takes them.  No derivative: an input that requires one is refused outside
+    torch.no_grad (so it is by fp8_matmul and orthogonalise)."""
     _matrix(x, "x", _WIDE)
     if block_rows not in (1, _BLOCK):
         raise ValueError("block_rows must be 1 or 128")
@@ -354,6 +367,7 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
         _matrix(minus, "minus", (torch.float32,), device=x.device)
         if minus.shape != x.shape:
             raise ValueError("minus must have the shape of x")
+    _no_gradient("fp8_quantise", x, minus)
     return _call(x.device, stream, _fp8_quantise, x, block_rows, dtype, minus, layout)
 
 
@@ -401,6 +415,7 @@ def fp8_matmul(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b:
     (N, Kb), args_b = _scaled(b, scale_b, "b", device)
     if K != Kb:
         raise ValueError("a and b must have the same number of columns")
+    _no_gradient("fp8_matmul", a, b, out)
     if out is None:
         if out_dtype not in _WIDE:
             raise TypeError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
@@ -417,6 +432,7 @@ def _fp8_matmul(args_a, args_b, M, N, K, alpha, out_dtype, out, device, st):
         out, ld = _empty((M, N), (N, 1), dtype=out_dtype, device=device), N
     else:
         out_dtype, ld = out.dtype, _ld(out)
+        _changed(out)
     rc = load().bcjr_fp8_matmul(*args_a, *args_b, M, N, K, float(alpha), out.data_ptr(), _TYPES[out_dtype], ld, st)
     _check(rc, "bcjr_fp8_matmul")
     return out
@@ -449,6 +465,7 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = 
     _matrix(g, "g", _WIDE, ndim=g.dim())
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float16")
+    _no_gradient("orthogonalise", g)
     return _call(g.device, stream, _orthogonalise, g, int(steps), _coeffs(coeffs, steps), eps, out_dtype)
 
 
@@ -470,7 +487,8 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: f
     momentum = mu momentum + grad; u = grad + mu momentum (or momentum without
     nesterov); w = (1 - lr weight_decay) w - lr scale orthogonalise(u), the last within
     about 1e-3 in the 2-norm.
-    ``scale`` defaults to sqrt(max(1, rows / cols)).  The three must not share memory."""
+    ``scale`` defaults to sqrt(max(1, rows / cols)).  The three must not share memory.
+    An optimizer's step: ``w`` may require a gradient, none is recorded."""
     _matrix(w, "w", (torch.float32,))
     _matrix(grad, "grad", _WIDE, device=w.device)
     _matrix(momentum, "momentum", (torch.float32,), device=w.device)
@@ -491,4 +509,5 @@ def _muon_step(w, grad, momentum, lr, mu, nesterov, weight_decay, scale, steps, 
                                _ld(momentum), rows, cols, float(lr), float(mu), nesterov, float(weight_decay), float(scale), steps,
                                coeffs, float(eps), st)
     _check(rc, "bcjr_muon_step")
+    _changed(w, momentum)
     return w, momentum

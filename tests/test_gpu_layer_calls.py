@@ -56,3 +56,41 @@ def test_matrices_between_one_anothers_rows_are_apart():
     lib.muon_step(w, g, m, 0.1)
     finished()
     assert torch.equal(w, want[0]) and torch.equal(m, want[1])
+
+
+# ---------------------------------------------------------------- autograd
+
+def test_results_without_a_gradient_are_refused():
+    x = randn(20, 40, seed=6).requires_grad_()
+    y = x.detach()
+    q, s = lib.fp8_quantise(y)
+    for call in (lambda: lib.fp8_quantise(x), lambda: lib.fp8_quantise(y, minus=x), lambda: lib.orthogonalise(x),
+                 lambda: lib.fp8_matmul(q, s, q, s, out=torch.zeros(20, 20, device=DEV, requires_grad=True))):
+        with pytest.raises(RuntimeError, match="no derivative"):
+            call()
+    with torch.no_grad():
+        assert torch.equal(lib.fp8_quantise(x)[0].view(torch.uint8), q.view(torch.uint8))
+        assert torch.equal(lib.orthogonalise(x), lib.orthogonalise(y))
+    finished()
+
+
+def test_a_step_on_a_parameter_is_seen_by_autograd():
+    """A graph that saved the weights does not go back with the changed ones."""
+    w = torch.nn.Parameter(randn(20, 40, seed=7))
+    m = torch.zeros(20, 40, device=DEV)
+    loss = (w * w).sum()
+    loss.backward()
+    kept = (w * w).sum()
+    before = (w._version, m._version)
+    lib.muon_step(w, w.grad, m, 0.1)
+    assert w._version > before[0] and m._version > before[1] and w.requires_grad and w.is_leaf
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        kept.backward()
+    q, s = lib.fp8_quantise(m)
+    out = torch.zeros(20, 20, device=DEV)
+    lib.fp8_matmul(q, s, q, s, out=out)
+    assert out._version > 0
+    with torch.inference_mode():
+        v = torch.ones(20, 40, device=DEV)
+        lib.muon_step(v, v * 2, torch.zeros_like(v), 0.1)
+    finished()
