@@ -438,14 +438,21 @@ def _fp8_matmul(args_a, args_b, M, N, K, alpha, out_dtype, out, device, st):
     return out
 
 
+def _steps(steps) -> int:
+    """A whole number of steps; what does not fit 32 bits as the limit that the library refuses."""
+    if steps != steps or int(steps) != steps:
+        raise ValueError("steps must be a whole number")
+    return max(-1, min(int(steps), 1 << 16))
+
+
 def _coeffs(coeffs, steps: int):
     """(a, b, c) for every step, or one triple for each, as a C array; None for the default."""
     if coeffs is None:
         return None
     flat = [float(v) for t in coeffs for v in (t if isinstance(t, (tuple, list)) else (t,))]
     if len(flat) == 3:
-        flat = flat * steps
-    if len(flat) != 3 * steps:
+        flat = flat * max(steps, 1)
+    if len(flat) != 3 * max(steps, 1):
         raise ValueError("coeffs must be (a, b, c) or one (a, b, c) for each step")
     return (ctypes.c_float * len(flat))(*flat)
 
@@ -466,7 +473,8 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = 
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float16")
     _no_gradient("orthogonalise", g)
-    return _call(g.device, stream, _orthogonalise, g, int(steps), _coeffs(coeffs, steps), eps, out_dtype)
+    steps = _steps(steps)
+    return _call(g.device, stream, _orthogonalise, g, steps, _coeffs(coeffs, steps), eps, out_dtype)
 
 
 def _orthogonalise(g, steps, coeffs, eps, out_dtype, st):
@@ -499,8 +507,9 @@ def muon_step(w: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: f
     rows, cols = w.shape
     if scale is None:
         scale = math.sqrt(max(1.0, rows / cols)) if cols else 1.0
+    steps = _steps(steps)
     return _call(w.device, stream, _muon_step, w, grad, momentum, lr, mu, int(bool(nesterov)), weight_decay, scale,
-                 int(steps), _coeffs(coeffs, steps), eps)
+                 steps, _coeffs(coeffs, steps), eps)
 
 
 def _muon_step(w, grad, momentum, lr, mu, nesterov, weight_decay, scale, steps, coeffs, eps, st):

@@ -94,3 +94,40 @@ def test_a_step_on_a_parameter_is_seen_by_autograd():
         v = torch.ones(20, 40, device=DEV)
         lib.muon_step(v, v * 2, torch.zeros_like(v), 0.1)
     finished()
+
+
+# ---------------------------------------------------------------- numbers
+
+def test_no_values_of_k_give_zeros_in_rows_of_any_length():
+    """Rows of more than 2^31 bytes too, and rows apart from one another."""
+    n = (1 << 29) + 8
+    for m, cols, keep in ((2, n, 0), (5, 33, 7), (1, 1 << 29, 0)):
+        a, b = (lib.fp8_quantise(torch.zeros(r, 0, device=DEV)) for r in (m, cols))
+        room = torch.full((m, cols + keep), 3.0, device=DEV)
+        lib.fp8_matmul(*a, *b, out=room[:, :cols])
+        finished()
+        assert not bool(room[:, :cols].any()) and bool((room[:, cols:] == 3).all())
+        del room
+        torch.cuda.empty_cache()
+
+
+def test_numbers_of_steps():
+    g = randn(20, 30, seed=8)
+    want = lib.orthogonalise(g, steps=3)
+    assert torch.equal(lib.orthogonalise(g, steps=3.0), want)
+    for bad in (2.5, float("nan")):
+        with pytest.raises(ValueError):
+            lib.orthogonalise(g, steps=bad)
+        with pytest.raises(ValueError):
+            lib.muon_step(g.clone(), g, torch.zeros_like(g), 0.1, steps=bad)
+    # what a 32-bit number would wrap around to one in range
+    for many in (65, 2 ** 31, 2 ** 32 + 5, 2 ** 70):
+        for coeffs in (None, (1.875, -1.25, 0.375)):
+            with pytest.raises(lib.BcjrError) as e:
+                lib.orthogonalise(g, steps=many, coeffs=coeffs)
+            assert e.value.status == lib.BCJR_ERR_UNSUPPORTED
+    for few in (0, -1, -2 ** 32 + 5):
+        with pytest.raises(lib.BcjrError) as e:
+            lib.orthogonalise(g, steps=few)
+        assert e.value.status == lib.BCJR_ERR_INVALID_ARG
+    finished()
