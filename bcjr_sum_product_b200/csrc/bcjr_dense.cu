@@ -268,15 +268,28 @@ int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st)
 
 constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 
+// The coefficients of each step, and the largest |a + b t + c t^2| that it can reach, by which it can amplify what an
+// earlier one left in X.
+struct Steps {
+  int count;
+  float co[3 * kMaxSteps], reach[kMaxSteps];
+};
+
 // The iterates and polynomials are kept in fp16 with headroom for entries up to
 // 16; the singular values of u / |u| lie in [0, 1].  False if, sampled over the
 // interval that each step can reach, the coefficients drive a singular value
-// above 2 or |a + b t + c t^2| above 8.  `reach`: the largest of the latter for each step,
-// by which the step can amplify what an earlier one left in X.
-bool coeffs_bounded(const float* co, int steps, float* reach) {
+// above 2 or |a + b t + c t^2| above 8.  (Muon's own are known: a + b t + c t^2 is
+// largest at t = 0.  Sampling them took 3.5 us of every call.)
+bool take_steps(const float* co, int steps, Steps* out) {
+  out->count = steps;
+  if (co == nullptr) {
+    for (int i = 0; i < 3 * steps; ++i) out->co[i] = kMuonCoeffs[i % 3];
+    for (int s = 0; s < steps; ++s) out->reach[s] = kMuonCoeffs[0];
+    return true;
+  }
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
-    const double a = co[3 * s], b = co[3 * s + 1], c = co[3 * s + 2];
+    const double a = out->co[3 * s] = co[3 * s], b = out->co[3 * s + 1] = co[3 * s + 1], c = out->co[3 * s + 2] = co[3 * s + 2];
     double most = 0.0, inner = 0.0;
     for (int i = 0; i <= 256; ++i) {
       const double x = top * i / 256.0, t = x * x;
@@ -284,7 +297,7 @@ bool coeffs_bounded(const float* co, int steps, float* reach) {
       inner = std::max(inner, std::fabs(a + t * (b + t * c)));
     }
     if (!(most <= 2.0) || !(inner <= 8.0)) return false;
-    if (reach != nullptr) reach[s] = (float)inner;
+    out->reach[s] = (float)inner;
     top = most;
   }
   return true;
@@ -294,12 +307,11 @@ struct Shape2 {
   int64_t batch, rows, cols;
 };
 
-int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps) {
+int check_iteration(const Shape2& sh, int steps, const float* coeffs, float eps, Steps* it) {
   if (sh.batch < 0 || sh.rows < 0 || sh.cols < 0) return BCJR_ERR_INVALID_ARG;
   if (steps < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return BCJR_ERR_INVALID_ARG;
   if (steps > kMaxSteps || sh.rows > kMaxMatrix || sh.cols > kMaxMatrix || sh.batch > kMaxBatch) return BCJR_ERR_UNSUPPORTED;
-  if (coeffs != nullptr && !coeffs_bounded(coeffs, steps, nullptr)) return BCJR_ERR_INVALID_ARG;
-  return BCJR_OK;
+  return take_steps(coeffs, steps, it) ? BCJR_OK : BCJR_ERR_INVALID_ARG;
 }
 
 // Stages of k of one product of iterates, but for those of a diagonal.
@@ -400,8 +412,9 @@ int launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
 
 // The whole iteration; `last` holds the epilogue of the last product (out, its layout and type, the weights'
 // factors) and says which by `epi`.  `precise`: every product with all second planes, for a result of more than 8 bits.
-int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps, const float* coeffs, int epi, bool precise,
-                      const G::Params& last, cudaStream_t st) {
+int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Steps& it, int epi, bool precise, const G::Params& last,
+                      cudaStream_t st) {
+  const int steps = it.count;
   int nsm = 0;
   if (int rc = sm_count(&nsm)) return rc;
   const bool tall = sh.rows > sh.cols;
@@ -412,16 +425,13 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
   const int64_t items = sh.rows * parts(sh.cols, Q::kSpan);
   u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
   const bool pairing = steps > 1 && worth_pairing(sh);
-  float flat[3 * kMaxSteps], reach[kMaxSteps];
-  for (int i = 0; i < 3 * steps; ++i) flat[i] = coeffs != nullptr ? coeffs[i] : kMuonCoeffs[i % 3];
-  coeffs_bounded(flat, steps, reach);
   // The product with X_s reads its second plane unless what one plane leaves out can grow at most four times in the steps
   // that are left (Muon's last step: 3.4): a result of rank 1, 512 x 512, is off by 0.2e-3 with both planes in all five
   // steps, 1.1e-3 in all but the last, 2.6e-3 in all but the last two, 0.15 in none.
   bool both[kMaxSteps];
   double gain = 1.0;
   for (int s = steps - 1; s >= 0; --s) {
-    gain *= reach[s];
+    gain *= it.reach[s];
     both[s] = precise || gain > 4.0;
   }
   const G::Second squares = precise ? G::ALL : G::DIAGONAL;
@@ -482,9 +492,9 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     q.second_r = q.second_c = squares;
     q.out = out;
     q.x = x;
-    q.fa = flat[3 * s];
-    q.fb = flat[3 * s + 1];
-    q.fc = flat[3 * s + 2];
+    q.fa = it.co[3 * s];
+    q.fb = it.co[3 * s + 1];
+    q.fc = it.co[3 * s + 2];
     return run_sym<G::POLY, false>(square(x), square(x), q, nsm, st);
   };
   const auto product = [&](__half* out, const __half* x, const __half* y) {
@@ -495,7 +505,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, int steps
     return run_sym<G::GRAM, false>(square(x), square(y), q, nsm, st);
   };
   for (int s = 0; s < steps && rc == BCJR_OK;) {
-    const bool two = pairing && s == 0 && reach[0] * reach[1] <= 15.f;   // their product stays within fp16's headroom
+    const bool two = pairing && s == 0 && it.reach[0] * it.reach[1] <= 15.f;   // their product stays within fp16's headroom
     // X along its rows (inner = columns): the Gram matrix of the shorter side
     // sums over the columns (wide, K-major) or over the rows (tall, MN-major)
     const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * 2, nx};
@@ -654,7 +664,8 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
                        int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out, int out_type,
                        int64_t ld_out, int64_t batch_stride_out, void* stream) {
   const Shape2 sh{batch, rows, cols};
-  int rc = check_iteration(sh, steps, coeffs, eps);
+  Steps it;
+  int rc = check_iteration(sh, steps, coeffs, eps, &it);
   if (rc) return rc;
   if (!is_wide(g_type) || (out_type != BCJR_F16 && out_type != BCJR_BF16)) return BCJR_ERR_INVALID_ARG;
   if (batch == 0 || rows == 0 || cols == 0) return BCJR_OK;
@@ -666,14 +677,15 @@ int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, i
   G::Params last{};
   last.out = out; last.ld_out = ld_out; last.batch_out = batch_stride_out; last.out_type = out_type;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return run_newton_schulz(sh, u, g_type, steps, coeffs, G::LAST, out_type != BCJR_BF16, last, st);
+  return run_newton_schulz(sh, u, g_type, it, G::LAST, out_type != BCJR_BF16, last, st);
 }
 
 int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int64_t ld_grad, float* momentum,
                    int64_t ld_momentum, int64_t rows, int64_t cols, float lr, float mu, int nesterov,
                    float weight_decay, float scale, int steps, const float* coeffs, float eps, void* stream) {
   const Shape2 sh{1, rows, cols};
-  int rc = check_iteration(sh, steps, coeffs, eps);
+  Steps it;
+  int rc = check_iteration(sh, steps, coeffs, eps, &it);
   if (rc) return rc;
   if (!is_wide(grad_type)) return BCJR_ERR_INVALID_ARG;
   if (!std::isfinite(lr) || !std::isfinite(mu) || !std::isfinite(weight_decay) || !std::isfinite(scale)) return BCJR_ERR_INVALID_ARG;
@@ -687,7 +699,7 @@ int bcjr_muon_step(float* w, int64_t ld_w, const void* grad, int grad_type, int6
   last.out = w; last.ld_out = ld_w;
   last.keep = (float)(1.0 - (double)lr * (double)weight_decay);
   last.rate = (float)((double)lr * (double)scale);
-  return run_newton_schulz(sh, u, grad_type, steps, coeffs, G::STEP, false, last, static_cast<cudaStream_t>(stream));
+  return run_newton_schulz(sh, u, grad_type, it, G::STEP, false, last, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -114,3 +114,10 @@ def test_updates_that_are_orthogonal_already(side):
     u = orthogonal_part(g)
     finished()
     assert relative(u, ref.newton_schulz(g)) <= bound(5, False)
+
+
+@pytest.mark.parametrize("rows,cols", [(200, 700), (1536, 6145)])
+def test_the_default_coefficients_are_those_given(rows, cols):
+    g = randn(rows, cols, seed=72)
+    assert torch.equal(lib.orthogonalise(g), lib.orthogonalise(g, coeffs=lib.MUON_COEFFS))
+    finished()
