@@ -370,8 +370,10 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
   if (p.rows > G::kRowsTile && t2 * parts(p.cols, 256) * p.batch * 4 >= nsm)
     return iter_pair<256, EPI, R_MN>(r, c, p, nsm, st);
-  if (p.cols <= 64 || t * parts(p.cols, 64) * p.batch <= 2 * nsm) return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
-  return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
+  // (one wide matrix that is not for pairs never has more tiles than that)
+  if constexpr (!(EPI == G::STEP && R_MN))
+    if (p.cols > 64 && t * parts(p.cols, 64) * p.batch > 2 * nsm) return iter_tile<128, EPI, R_MN>(r, c, p, nsm, st);
+  return iter_tile<64, EPI, R_MN>(r, c, p, nsm, st);
 }
 
 // Whether the first two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
