@@ -3,7 +3,8 @@ memory, gradients, numbers, streams and graphs."""
 import pytest
 import torch
 
-from bcjr_sum_product_b200 import lib
+from bcjr_sum_product_b200 import inputs as I
+from bcjr_sum_product_b200 import lib, qat
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -131,3 +132,49 @@ def test_numbers_of_steps():
             lib.orthogonalise(g, steps=few)
         assert e.value.status == lib.BCJR_ERR_INVALID_ARG
     finished()
+
+
+# ---------------------------------------------------------------- precision of a layer's loss
+
+def test_products_of_a_layers_loss():
+    """Against 64 bits: fp32; and 8-bit operands, whose errors are those of their codes: x and the residual off by at
+    most 2^-4 of an entry in e4m3 (in the 2-norm 2^-4 / sqrt(3) of the whole), R by 2^-9 as bf16 and by 2^-3 or 2^-4 as
+    codes; errors of a product's two sides add up as independent ones."""
+    tokens, out, inner = 512, 640, 1024
+    x, soft, target = randn(tokens, inner, seed=9), randn(out, inner, seed=10), randn(out, inner, seed=11)
+    r64 = x.double() @ (soft.double() - target.double()).t()
+    g64 = 2.0 / tokens * (r64.t() @ x.double())
+    off = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+    r, g = qat.layer_loss_fp32(soft, target, x)
+    assert off(r, r64) <= 2.0 ** -18 and off(g, g64) <= 2.0 ** -18
+    operands = qat.layer_operands(x)
+    errors = {}
+    for r_dtype, step in ((torch.float8_e5m2, 2.0 ** -3), (torch.float8_e4m3fn, 2.0 ** -4)):
+        r, g = qat.layer_loss(soft, target, operands, r_dtype=r_dtype)
+        code = 2.0 ** -4 / 3 ** 0.5
+        assert off(r, r64) <= code * 2 ** 0.5
+        assert off(g, g64) <= (2 * code ** 2 + (step / 3 ** 0.5) ** 2 + code ** 2) ** 0.5
+        errors[r_dtype] = off(g, g64)
+    assert errors[torch.float8_e4m3fn] < errors[torch.float8_e5m2]
+    finished()
+
+
+@pytest.mark.parametrize("products", ["e5m2", "e4m3", "fp32"])
+def test_driver_with_either_products(products):
+    shape, L, k, V = (64, 128), 8, 2, 1
+    target, c, _ = I.random_case(L, k, V, 128, 64, seed=45)
+    t, cb, x = target.to(DEV), c.to(DEV), randn(96, shape[1], seed=46)
+    out = qat.run(t, cb, L, k, V, 0.3, 0.1, 2, 1e-2, x=x, shape=shape, optimizer="muon", products=products)
+    w, m, losses = t.clone(), torch.zeros_like(t), []
+    for T in qat.anneal(0.3, 0.1, 2):
+        soft, _ = lib.soft_codeword(w, cb, L, k, V, T)
+        if products == "fp32":
+            r, g = qat.layer_loss_fp32(soft.view(shape), t.view(shape), x)
+        else:
+            r, g = qat.layer_loss(soft.view(shape), t.view(shape), qat.layer_operands(x),
+                                  r_dtype=torch.float8_e4m3fn if products == "e4m3" else torch.float8_e5m2)
+        losses.append(float(r.float().square().sum()) / 96)
+        gw, _ = lib.vjp(w, cb, L, k, V, T, g.reshape(w.shape))
+        lib.muon_step(w.view(shape), gw.view(shape), m.view(shape), 1e-2)
+    finished()
+    assert torch.equal(out["w"], w) and out["loss"] == pytest.approx(losses, rel=1e-5)

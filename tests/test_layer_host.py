@@ -141,3 +141,11 @@ def test_overlap_of_matrices():
             assert lib._overlap(p, q) == want
             seen.add(want)
     assert seen == {True, False}
+
+
+def test_products_of_the_driver():
+    w, c = torch.zeros(4, 8), torch.zeros(16)
+    with pytest.raises(ValueError):
+        qat.run(w, c, 4, 2, 1, 0.3, 0.1, 2, 1e-3, x=torch.zeros(5, 8), shape=(4, 8), products="bf16")
+    with pytest.raises(SystemExit):
+        qat.main(["--loss", "layer", "--products", "int8"])
