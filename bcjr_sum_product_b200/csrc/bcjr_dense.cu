@@ -200,8 +200,8 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
 }
 
 // Blocks of one tile: as many (1, 2, 4 or 8) as the tiles leave room for, each with at least four stages of k.  Exchanging
-// the sums costs about 2 us, a stage 0.2.  256 x 256 update (4 stages): 62 us unsplit, 73 split in two; 128 x 4096 (64
-// stages): 111 us unsplit, 66 in eight; two blocks on an SM instead of one make 512 x 2048 slower (89 to 105 us).
+// the sums costs about 2 us, a stage 0.2.  Updates of 128 x 4096: 143 us unsplit, 95 in up to eight; 512 x 2048: 138 and
+// 118; two blocks on an SM instead of one would make the latter slower again (with one plane 105 us against 89).
 int splits_for(int64_t tiles, int64_t stages, int nsm) {
   int s = 1;
   while (s < 8 && tiles * s * 2 <= nsm && stages >= s * 8) s *= 2;
@@ -336,11 +336,11 @@ int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStrea
   return launch_pair<G::F16, BN, MN, MN, EPI>(x, y, p, nsm, st);
 }
 // Pairs of SMs (tiles of 256 rows) where they have a quarter of the GPU's SMs' number of tiles to work on: from half of
-// that on 1024^2 takes 130 us instead of 108, with twice of it 2048^2 takes 245 instead of 216.  Never for matrices of at
-// most 128 rows, where half of every such tile is empty: 256 of 128 x 256 take 185 us in single blocks and 321 in pairs,
-// 1000 of 32 x 96 394 and 680; from 129 rows on pairs win (64 of 256 x 512: 171 us against 193).  Single blocks take 64
-// columns where those fill two blocks an SM at most (16 of 333 x 130: 86 us, at one block an SM 96), else 128 (256 of
-// 128 x 256: 185 us against 224).
+// that on 1024^2 takes 181 us instead of 143, with twice of it 2048^2 takes 340 instead of 303.  Never for matrices of at
+// most 128 rows, where half of every such tile is empty: 256 of 128 x 256 take 257 us in single blocks and 415 in pairs,
+// 1000 of 32 x 96 345 and 707; from 129 rows on pairs win (64 of 256 x 512: 237 us against 281).  Single blocks take 64
+// columns where those fill two blocks an SM at most, else 128 (256 of 128 x 256: 257 us against 306; 1000 of 32 x 96:
+// 345 against 495).
 template <int EPI, bool MN>
 int run_sym(const Operand& x, const Operand& y, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
@@ -363,8 +363,10 @@ int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStre
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
   return launch_pair<G::F16, BN, R_MN, false, EPI>(r, c, p, nsm, st);
 }
-// As for the symmetric products: pairs from a quarter (1024 x 2048: 135 us; from a tenth 141; 1024 x 4096 from a half:
-// 196 instead of 163), and not for 128 rows or fewer (1000 of 32 x 96: 394 us against 420, 64 of 128 x 128: 68 against 77).
+// As for the symmetric products: pairs from a quarter (from an eighth 1024 x 2048 takes 188 us instead of 175, from a half
+// 2048^2 325 instead of 303), and not for 128 rows or fewer (64 of 128 x 128: 91 us against 155).  Single blocks take 64
+// columns up to two blocks an SM (16 of 333 x 130: 119 us, up to one block an SM 136), else 128 (300 of 96 x 40: 209 us
+// against 219).
 template <int EPI, bool R_MN>
 int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cudaStream_t st) {
   const int64_t t = parts(p.rows, G::kRowsTile), t2 = parts(p.rows, 2 * G::kRowsTile);
@@ -378,8 +380,9 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
 
 // Whether the first two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
 // one Gram matrix of X and one product with X (two passes) instead of two, for three more products of the shorter
-// side's size.  Estimated from measured times: 5 us for each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s
-// for Gram matrices (whole flops), products with X and small symmetric products.
+// side's size (1536 x 6145: 510 us against 566; 2048 x 8192: 772 against 820).  Estimated from measured times: 5 us for
+// each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s for Gram matrices (whole flops), products with X and
+// small symmetric products.
 // Only the first two, and from 512 rows on.  A rounding N of P turns a direction of eigenvalue t into others by
 // |N u| (f(t) - f(0)) / t, with f = B2 B1 from 11.9 at t = 0 to 0.5 at t = 1.  |N u| is about 2^-12 t sqrt(rank / m), and
 // at first t is at most 1 / rank: next to nothing (512 rows or more: as one step at a time; 16 x 3652: 2.3e-3 against

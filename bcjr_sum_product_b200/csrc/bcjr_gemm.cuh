@@ -331,6 +331,13 @@ __device__ __forceinline__ void stage_products(uint32_t acc, uint32_t a, uint32_
 // ------------------------------------------------------------ small products
 
 constexpr int kTileThreads = 576;
+// Blocks on an SM that the registers must leave room for.  Two (56 registers) for what runs in more blocks than there
+// are SMs.  64-column tiles of symmetric products seldom do and are faster with 87 or 96 registers (512 x 2048: 118 us
+// against 124; 16 of 333 x 130: 111 against 119; products with X in one block an SM: 120); 128 columns of a polynomial
+// in 56 spill (256 of 128 x 256: 276 us against 259), so the compiler chooses (76).
+__host__ __device__ constexpr int tile_blocks(int bn, int epi) {
+  return bn < 128 && (epi == GRAM || epi == POLY) ? 1 : epi == POLY ? 0 : 2;
+}
 
 template <int KIND, int BN>
 struct TileShape {
@@ -356,9 +363,10 @@ struct TileShape {
 // the order of the ranks, so the result does not depend on timing.  What bounds it
 // is latency, not a pipe: of the 6 us of a product of 512 x 512 x 2048 the first
 // copy takes 0.8, eight stages 1.7 (64 bytes a clock and SM from L2), the exchange
-// 2.0, the stores 0.9.  One token through 8192 x 2048 (17 MB): 6.5 us, 2.6 TB/s.
+// 2.0, the stores 0.9.  One token through 8192 x 2048 (17 MB): 6.5 us, 2.6 TB/s of L2
+// (calls in a row on the same operands); 11.6 us, 1.5 TB/s, from HBM.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
-__global__ void __launch_bounds__(kTileThreads) tile_kernel(const __grid_constant__ CUtensorMap map_r,
+__global__ void __launch_bounds__(kTileThreads, tile_blocks(BN, EPI)) tile_kernel(const __grid_constant__ CUtensorMap map_r,
                                                              const __grid_constant__ CUtensorMap map_c, const Params p) {
   using S = TileShape<KIND, BN>;
   constexpr bool SYM = EPI == GRAM || EPI == POLY;

@@ -121,3 +121,13 @@ def test_the_default_coefficients_are_those_given(rows, cols):
     g = randn(rows, cols, seed=72)
     assert torch.equal(lib.orthogonalise(g), lib.orthogonalise(g, coeffs=lib.MUON_COEFFS))
     finished()
+
+
+@pytest.mark.parametrize("shape", [(32767, 3, 5), (1, 1, 65536), (1, 65536, 1), (1, 65536, 9), (2, 7, 65536)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16])
+def test_largest_extents(shape, out_dtype):
+    g = randn(*shape, seed=73)
+    out = lib.orthogonalise(g, out_dtype=out_dtype)
+    finished()
+    # single matrices of a batch this large may have roundings that agree: of at most five values of k
+    assert relative(out, ref.newton_schulz(g)) <= 3 * (bound(5, False) + HALF_STEP[out_dtype] / math.sqrt(3))

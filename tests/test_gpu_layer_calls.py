@@ -178,3 +178,119 @@ def test_driver_with_either_products(products):
         lib.muon_step(w.view(shape), gw.view(shape), m.view(shape), 1e-2)
     finished()
     assert torch.equal(out["w"], w) and out["loss"] == pytest.approx(losses, rel=1e-5)
+
+
+# ---------------------------------------------------------------- values of codes and scales
+
+E8M0 = torch.float8_e8m0fnu
+
+
+def scaled(q, block_rows):
+    """Scales of 1 for codes of any value."""
+    rows, cols = q.shape
+    return torch.full((-(-rows // block_rows), -(-cols // 128)), 127, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 40, 300), (70, 140, 300), (1030, 2000, 600)])
+def test_scales_that_are_nan_spoil_what_they_enter(m, n, k):
+    """Over finite codes, and over zeros."""
+    a, b = (randn(r, k, seed=s).to(torch.float8_e4m3fn) for r, s in ((m, 12), (n, 13)))
+    room = [torch.zeros(t.shape[0], 608, dtype=torch.uint8, device=DEV) for t in (a, b)]
+    for r, t in zip(room, (a, b)):
+        r[:, :k] = t.view(torch.uint8)
+    a, b = (r.view(torch.float8_e4m3fn)[:, :k] for r in room)
+    room[0][3, 128:256] = 0
+    sa, sb = scaled(a, 1), scaled(b, 128)
+    sa[3, 1] = 255
+    sb[n // 128, k // 128] = 255                       # the last rows' last values
+    y = lib.fp8_matmul(a, sa.view(E8M0), b, sb.view(E8M0), out_dtype=torch.float32)
+    finished()
+    want = torch.zeros(m, n, dtype=torch.bool, device=DEV)
+    want[3] = True
+    want[:, n // 128 * 128:] = True
+    assert torch.equal(torch.isnan(y), want)
+    assert bool(torch.isfinite(y[~want]).all())
+
+
+@pytest.mark.parametrize("m,n", [(5, 40), (1030, 2000)])
+def test_scales_at_the_ends_of_their_range(m, n):
+    """2^-127 and 2^127 are scales like any other; what the products' sums make of them stays in fp32."""
+    k = 256
+    x, w = randn(m, k, seed=14), randn(n, k, seed=15)
+    a, b = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+    one = torch.full((m, 2), 127, dtype=torch.uint8, device=DEV), torch.full((-(-n // 128), 2), 127, dtype=torch.uint8, device=DEV)
+    plain = lib.fp8_matmul(a, one[0].view(E8M0), b, one[1].view(E8M0), out_dtype=torch.float32)
+    for low, high in ((0, 254), (254, 0)):
+        sa, sb = torch.full_like(one[0], low), torch.full_like(one[1], high)
+        y = lib.fp8_matmul(a, sa.view(E8M0), b, sb.view(E8M0), out_dtype=torch.float32)
+        assert torch.equal(y, plain)
+    finished()
+
+
+def test_infinite_codes():
+    """e5m2 has infinities: theirs is the sum's, and with a zero or the other sign NaN."""
+    a, b = torch.ones(3, 16, device=DEV), torch.ones(4, 16, device=DEV)
+    a[1, 5] = float("inf")
+    b[2, 5] = 0.0
+    b[3, 5] = -1.0
+    q, r = a.to(torch.float8_e5m2), b.to(torch.float8_e4m3fn)
+    y = lib.fp8_matmul(q, scaled(q, 1).view(E8M0), r, scaled(r, 1).view(E8M0), out_dtype=torch.float32)
+    finished()
+    inf = float("inf")
+    assert torch.equal(y[0], torch.tensor([16.0, 16.0, 15.0, 14.0], device=DEV)) and torch.equal(y[0], y[2])
+    assert y[1, 0] == inf and y[1, 1] == inf and torch.isnan(y[1, 2]) and y[1, 3] == -inf
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+def test_a_graph_of_two_streams():
+    """Calls on both sides of a fork inside a capture, and after the join; replayed with new values."""
+    x, w, m = randn(300, 520, seed=16), randn(700, 520, seed=17), torch.zeros(300, 520, device=DEV)
+    big = randn(1100, 1200, seed=18)
+
+    def work(side):
+        main = torch.cuda.current_stream()
+        qx = lib.fp8_quantise(x)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            o = lib.orthogonalise(big)
+            qw = lib.fp8_quantise(w, 128)
+        p = lib.orthogonalise(x)
+        main.wait_stream(side)
+        y = lib.fp8_matmul(*qx, *qw)
+        lib.muon_step(x, p, m, 0.1)
+        return o, p, y
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work(side)
+    for turn in range(3):
+        start = randn(300, 520, seed=20 + turn)
+        x.copy_(start)
+        m.fill_(0.5)
+        big.copy_(randn(1100, 1200, seed=30 + turn))
+        want = [t.clone() for t in work(torch.cuda.Stream())] + [x.clone(), m.clone()]
+        x.copy_(start)
+        m.fill_(0.5)
+        torch.cuda.synchronize()
+        graph.replay()
+        finished()
+        for got, wanted in zip((*out, x, m), want):
+            assert torch.equal(got, wanted)
+
+
+def test_a_batch_of_one_matrix_again_and_again():
+    """A broadcast batch, windows that overlap, and rows of one matrix of a batch apart from the next."""
+    g = randn(40, 90, seed=19)
+    one = lib.orthogonalise(g)
+    many = lib.orthogonalise(g.expand(5, 40, 90))
+    windows = lib.orthogonalise(g.as_strided((3, 20, 90), (10 * 90, 90, 1)))
+    apart = lib.orthogonalise(torch.stack([g, g], 1).transpose(0, 1))
+    finished()
+    # (the number of blocks that sum a norm depends on the batch)
+    for got in (*many, *apart):
+        assert float((got.float() - one.float()).norm()) <= 2.0 ** -8 * float(one.float().norm())
+    for i in range(3):
+        assert float((windows[i].float() - lib.orthogonalise(g[10 * i:10 * i + 20]).float()).norm()) <= 2.0 ** -8 * 20 ** 0.5
