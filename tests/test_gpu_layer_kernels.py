@@ -1,14 +1,12 @@
 """Every kernel of the layer-wise QAT operators on values, over several blocks of k, several
 tiles and ragged ends, with the kernel that each case takes read from the profiler: a
 change of the rules that choose them does not silently leave one untested."""
-import math
-
 import pytest
 import torch
 
 import layer_reference as ref
 from bcjr_sum_product_b200 import lib
-from test_gpu_layer_accuracy import bound
+from test_gpu_layer_accuracy import bound, rounded
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -170,7 +168,7 @@ def test_batches_on_wide_single_blocks(batch, rows, cols, widths, out_dtype):
     finished()
     for end, width, r_mn in widths:
         assert kernel("tile", 0, width, r_mn, end == GRAM and r_mn, end) in names, names
-    assert relative(out, ref.newton_schulz(g)) <= bound(5, False) + HALF_STEP[out_dtype] / math.sqrt(3)
+    assert relative(out, ref.newton_schulz(g)) <= rounded(bound(5, False), out_dtype)
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F16])
@@ -180,4 +178,4 @@ def test_orthogonalise_in_bands(out_dtype):
     out, names = launched(lambda: lib.orthogonalise(g, out_dtype=out_dtype))
     finished()
     assert kernel("pair", 0, 256, True, False, ITER) in names
-    assert relative(out, ref.newton_schulz(g)) <= bound(5, True) + HALF_STEP[out_dtype] / math.sqrt(3)
+    assert relative(out, ref.newton_schulz(g)) <= rounded(bound(5, True), out_dtype)
