@@ -192,10 +192,12 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), &done, S::kSmem))) return rc;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
   // The pairs that run together work on neighbouring columns of all of R, which then has to stay in
-  // L2 (126 MB); a larger R is taken in bands of 16 tiles (8-bit 8192 x 8192 x 8192: 492 -> 446 us;
-  // with k = 2048, where R is 16 MB, bands cost 3 %).
+  // L2 (126 MB); a larger R, second plane included, is taken in bands of 16 tiles (8-bit 8192 x 8192 x 8192: 492 -> 446
+  // us; orthogonalisation of 2048 x 8192, X in two planes of 34 MB: 707 -> 671; 8-bit with k = 2048, where R is 16 MB, bands
+  // cost 3 %).
   G::Params pb = p;
-  pb.band = r.inner * r.outer * elem > ((int64_t)48 << 20) ? std::min(p.tiles_r, 16) : p.tiles_r;
+  const int64_t bytes = r.inner * r.outer * elem * (p.second_r == G::ALL ? 2 : 1);
+  pb.band = bytes > ((int64_t)48 << 20) ? std::min(p.tiles_r, 16) : p.tiles_r;
   return launch(kern, 2 * pairs, 1, G::kPairThreads, S::kSmem, 2, mr, mc, pb, st);
 }
 

@@ -625,10 +625,12 @@ struct PairShape {
 // alternate between two halves of tensor memory, and warps 4 to 11 store one
 // tile while the next is computed.  Warps 2 and 3 bring the scales.  A stage holds
 // two blocks of k, since every commit (the hand-back of a stage) makes the tensor
-// cores pause: about 0.13 us each, measured.  8-bit 8192 x 8192 x 2048: 121 us in a
-// row, 2.27 PFLOP/s (147 us with inputs and outputs that L2 does not hold); what
-// bounds it is the SMs' way to L2 (60 KB a stage and block at 64 bytes a clock, about
-// as long as the products) with the stores on the same way (without them 106 us).
+// cores pause: about 0.13 us each, measured.  8-bit 8192 x 8192 x 2048: 120 us in a
+// row, 2.29 PFLOP/s (145 us with inputs and outputs that L2 does not hold).  No unit is
+// at its limit: the tensor pipe is active 61 % of the time, L2 delivers 9.8 TB/s (43 % of
+// its throughput, a third of the SMs' way to it).  The rest is waiting: eight commits a
+// tile and sixteen tiles (17 us), the stores on the operands' way (without them 106 us),
+// the first stages of each tile, and a clock of 1.6 GHz under the power limit.
 // fp16 256 x 256 tiles: 0.29 us for 64 values of k, the tensor cores' own rate 0.27.
 template <int KIND, int BN, bool R_MN, bool C_MN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ CUtensorMap map_r,
