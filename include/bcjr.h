@@ -270,8 +270,8 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * rounding left as a second such value (22 bits).  For a bf16 out these are the
  * iterates that are multiplied (but the last, which 11 bits hold well enough) and
  * the diagonals, which keeps out within about 1e-3 of the exact iteration in the
- * 2-norm (2e-3 at most), less than its own rounding, whatever the singular values
- * of G; for an fp16 out all of them (three times the products), which leaves 1e-4
+ * 2-norm (2e-3 at most in Muon's five steps), less than its own rounding, whatever
+ * the singular values of G; for an fp16 out all of them (three times the products), which leaves 1e-4
  * before it is rounded, or where few directions carry G what the fp32 sums leave
  * in the others and the steps amplify: 2e-4 (512 x 512) to 1.1e-3 (2048 x 2048).
  *   g       [batch][rows][cols]  fp32, fp16 or bf16 (input)
@@ -283,8 +283,9 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * gives zeros (eps > 0); NaN or infinities make that matrix NaN.  Entries of X_0
  * below 2^-36 vanish (so does a G whose norm is that far below eps).  Steps amplify
  * the directions whose singular values are small against ||G||_F (Muon's default:
- * up to 485 times), what G itself holds there, such as the rounding of a bf16 G,
- * included.
+ * 3.4 times each, five of them 485 times), and with them what is there of roundings:
+ * of G itself, if it is bf16, and of 22 bits, so that with more than about ten
+ * such steps the directions that G does not have are no longer small.
  */
 BCJR_API int bcjr_orthogonalise(const void* g, int g_type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g,
                                 int64_t batch_stride_g, int steps, const float* coeffs, float eps, void* out,
