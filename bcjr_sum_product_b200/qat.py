@@ -211,8 +211,8 @@ def main(argv: Optional[List[str]] = None) -> int:
     if a.loss == "layer" or a.optimizer == "muon":
         # whole rows of the workload's first matrix
         n, cols = min(a.seqs, wl.n_seq) * wl.seq_len, wl.matrices[0][1]
-        if n % cols or n > wl.matrices[0][0] * cols:
-            ap.error(f"--seqs must make whole rows of {cols} weights of the first matrix (at most {wl.matrices[0][0]} rows)")
+        if n < 1 or n % cols or n > wl.matrices[0][0] * cols:
+            ap.error(f"--seqs must make whole rows of {cols} weights of the first matrix (1 to {wl.matrices[0][0]} rows)")
         if a.tokens < 1:
             ap.error("--tokens must be positive")
         shape = (n // cols, cols)

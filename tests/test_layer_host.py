@@ -149,3 +149,11 @@ def test_products_of_the_driver():
         qat.run(w, c, 4, 2, 1, 0.3, 0.1, 2, 1e-3, x=torch.zeros(5, 8), shape=(4, 8), products="bf16")
     with pytest.raises(SystemExit):
         qat.main(["--loss", "layer", "--products", "int8"])
+
+
+def test_command_without_rows(capsys):
+    for seqs in ("0", "-8", "-16"):
+        for argv in (["--loss", "layer"], ["--optimizer", "muon"]):
+            with pytest.raises(SystemExit):
+                qat.main(["--workload", "tiny", "--seqs", seqs, *argv])
+    capsys.readouterr()
