@@ -419,6 +419,9 @@ int launch_update(const Q::UpdateParams& u, int64_t batch, cudaStream_t st) {
 
 // The whole iteration; `last` holds the epilogue of the last product (out, its layout and type, the weights'
 // factors) and says which by `epi`.  `precise`: every product with all second planes, for a result of more than 8 bits.
+// So are matrices of fewer than 32 rows (or columns), too few for roundings to average out (2 x 5 otherwise up to 1e-2, 8 x 8
+// 4e-3, 32 x 32 1.4e-3): they have one block of k, so it is a stage or two more.  Not the Gram matrix of a long one, where
+// X's roundings average out along the other side (1024: 2^-11 / 55).
 int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Steps& it, int epi, bool precise, const G::Params& last,
                       cudaStream_t st) {
   const int steps = it.count;
@@ -435,13 +438,14 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
   // The product with X_s reads its second plane unless what one plane leaves out can grow at most four times in the steps
   // that are left (Muon's last step: 3.4): a result of rank 1, 512 x 512, is off by 0.2e-3 with both planes in all five
   // steps, 1.1e-3 in all but the last, 2.6e-3 in all but the last two, 0.15 in none.
+  const bool all = precise || m < 32, gram_all = precise || (all && std::max(sh.rows, sh.cols) < 1024);
   bool both[kMaxSteps];
   double gain = 1.0;
   for (int s = steps - 1; s >= 0; --s) {
     gain *= it.reach[s];
-    both[s] = precise || gain > 4.0;
+    both[s] = all || gain > 4.0;
   }
-  const G::Second squares = precise ? G::ALL : G::DIAGONAL;
+  const G::Second squares = all ? G::ALL : G::DIAGONAL;
   __half *x0, *x1, *pp, *bb, *tt;
   const int64_t next = up(sh.batch * 2 * np, 128);   // from one square matrix to the next
   double* partial;
@@ -466,7 +470,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
   u.batch_x = 2 * nx;
   u.plane_x = nx;
   u.planes = both[0] ? 2 : 1;
-  if (!precise) {
+  if (!all) {
     u.squares = pp + np;
     u.ld_s = ld_p;
     u.batch_s = 2 * np;
@@ -518,7 +522,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
     const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * 2, nx};
     G::Params gram = p;
     gram.k = (int)(tall ? sh.rows : sh.cols);
-    gram.second_r = gram.second_c = precise ? G::ALL : G::NONE;
+    gram.second_r = gram.second_c = gram_all ? G::ALL : G::NONE;
     gram.out = pp;
     rc = tall ? run_sym<G::GRAM, true>(x, x, gram, nsm, st) : run_sym<G::GRAM, false>(x, x, gram, nsm, st);
     if (rc || (rc = polynomial(bb, pp, s))) break;

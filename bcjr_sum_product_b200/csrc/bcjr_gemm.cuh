@@ -66,9 +66,10 @@ enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 //     a step of a (rank 1, 1536 x 6145, two steps at once: 1 %).  Of the second
 //     planes' blocks of 256 on the diagonal, zeros but for it, a product takes those of
 //     its tile's own rows: one to four blocks of k more.
-// So held, a result is within 1.3e-3 of the exact iteration in the 2-norm whatever its
-// singular values (1.8e-3 at 7 x 9; half of that for updates of full rank).  For results of more than 8 bits
-// every product takes all second planes: R0 C0 + R0 C1 + R1 C0.
+// So held, a result is within 1.4e-3 of the exact iteration in the 2-norm whatever its
+// singular values (half of that for updates of full rank).  For results of more than
+// 8 bits, and for matrices of few rows, every product takes all second planes:
+// R0 C0 + R0 C1 + R1 C0.
 constexpr float kIterScale = 4096.f;
 
 // Which part of an operand's or a result's second plane counts.

@@ -136,3 +136,25 @@ def test_largest_extents(shape, out_dtype):
     finished()
     # single matrices of a batch this large may have roundings that agree: of at most five values of k
     assert relative(out, ref.newton_schulz(g)) <= 3 * rounded(bound(5, False), out_dtype)
+
+
+# ---------------------------------------------------------------- few rows
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (2, 2), (2, 5), (5, 2), (3, 3), (4, 9), (8, 8), (30, 8), (16, 16), (31, 31),
+                                       (7, 1100), (3000, 5)])
+def test_every_matrix_of_few_rows(rows, cols):
+    """Too few entries for roundings to average out: the worst of thousands of matrices.  An entry of 22 bits is off
+    by at most 2^-22, sums over few values of k by five steps of 2^-23, and what is added to X grows by what is
+    left of the five steps, 682 times in all; the Gram matrix of a long one has X's 11 bits averaged along it, counted
+    three times a step as above."""
+    n = min(32767, 1000000 // (rows * cols))
+    g = randn(n, rows, cols, seed=rows + 40 * cols)
+    want = ref.newton_schulz(g)
+    long_side = max(rows, cols)
+    tol = 682 * (2.0 ** -22 + 5 * 2.0 ** -23) + (15 * 2.0 ** -11 / math.sqrt(3 * long_side) if long_side >= 1024 else 0.0)
+    out, fine = lib.orthogonalise(g), lib.orthogonalise(g, out_dtype=torch.float16)
+    finished()
+    assert relative(out, want) <= tol + HALF_STEP[torch.bfloat16]
+    assert relative(fine, want) <= tol + HALF_STEP[torch.float16]
+    for i in range(0, n, max(1, n // 40)):
+        assert relative(orthogonal_part(g[i]), want[i]) <= tol
