@@ -158,3 +158,29 @@ def test_every_matrix_of_few_rows(rows, cols):
     assert relative(fine, want) <= tol + HALF_STEP[torch.float16]
     for i in range(0, n, max(1, n // 40)):
         assert relative(orthogonal_part(g[i]), want[i]) <= tol
+
+
+@pytest.mark.parametrize("rows,cols", [(512, 512), (200, 700), (1536, 6145), (6200, 1500), (333, 130)])
+@pytest.mark.parametrize("strong,ratio", [(1, 1e2), (1, 1e4), (6, 30.0), (40, 1e3)])
+def test_few_directions_far_above_the_rest(rows, cols, strong, ratio):
+    """The rest of full rank below them: where the result lives after five steps depends on how far."""
+    g = low_rank(rows, cols, strong, seed=91)
+    rest = randn(rows, cols, seed=93)
+    g = g + rest * float(torch.linalg.vector_norm(g) / torch.linalg.vector_norm(rest)) / ratio
+    want = ref.newton_schulz(g)
+    u = orthogonal_part(g)
+    finished()
+    assert relative(u, want) <= bound(5, min(rows, cols) >= 1500)
+
+
+def test_power_law_spectra():
+    """Singular values i^-p."""
+    for rows, cols in ((300, 500), (1100, 1000)):
+        k = min(rows, cols)
+        q, _ = torch.linalg.qr(randn(rows, k, seed=94).double())
+        r, _ = torch.linalg.qr(randn(cols, k, seed=95).double())
+        for p in (0.25, 0.5, 1.0, 2.0, 4.0):
+            g = ((q * torch.arange(1, k + 1, device=DEV).double() ** -p) @ r.mT).float().contiguous()
+            u = orthogonal_part(g)
+            finished()
+            assert relative(u, ref.newton_schulz(g)) <= bound(5, False)
