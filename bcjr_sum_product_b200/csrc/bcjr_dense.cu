@@ -193,8 +193,8 @@ int launch_pair(const Operand& r, const Operand& c, const G::Params& p, int nsm,
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles * p.batch, nsm / 2);
   // The pairs that run together work on neighbouring columns of all of R, which then has to stay in
   // L2 (126 MB); a larger R, second plane included, is taken in bands of 16 tiles (8-bit 8192 x 8192 x 8192: 492 -> 446
-  // us; orthogonalisation of 2048 x 8192, X in two planes of 34 MB: 707 -> 671; 8-bit with k = 2048, where R is 16 MB, bands
-  // cost 3 %).
+  // us; fp16 orthogonalisation of 2048 x 8192, X in two planes of 34 MB: 1475 -> 1435; 8-bit with k = 2048, where R is 16
+  // MB, bands cost 3 %).
   G::Params pb = p;
   const int64_t bytes = r.inner * r.outer * elem * (p.second_r == G::ALL ? 2 : 1);
   pb.band = bytes > ((int64_t)48 << 20) ? std::min(p.tiles_r, 16) : p.tiles_r;
@@ -233,7 +233,7 @@ int matmul_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaSt
 int run_matmul(const Operand& r, const Operand& c, G::Params p, cudaStream_t st) {
   int nsm = 0;
   if (int rc = sm_count(&nsm)) return rc;
-  p.batch = p.planes = 1;
+  p.batch = p.planes_r = p.planes_c = 1;
   if (p.cols <= 16) return matmul_tile<16>(r, c, p, nsm, st);
   if (p.cols <= 32) return matmul_tile<32>(r, c, p, nsm, st);
   if (p.cols <= 64) return matmul_tile<64>(r, c, p, nsm, st);
@@ -338,7 +338,7 @@ int sym_pair(const Operand& x, const Operand& y, G::Params p, int nsm, cudaStrea
   return launch_pair<G::F16, BN, MN, MN, EPI>(x, y, p, nsm, st);
 }
 // Pairs of SMs (tiles of 256 rows) where they have a quarter of the GPU's SMs' number of tiles to work on: from half of
-// that on 1024^2 takes 181 us instead of 143, with twice of it 2048^2 takes 340 instead of 303.  Never for matrices of at
+// that on 1024^2 takes 165 us instead of 127, with twice of it 2048^2 takes 339 instead of 272.  Never for matrices of at
 // most 128 rows, where half of every such tile is empty: 256 of 128 x 256 take 257 us in single blocks and 415 in pairs,
 // 1000 of 32 x 96 345 and 707; from 129 rows on pairs win (64 of 256 x 512: 237 us against 281).  Single blocks take 64
 // columns where those fill two blocks an SM at most, else 128 (256 of 128 x 256: 257 us against 306; 1000 of 32 x 96:
@@ -365,8 +365,8 @@ int iter_pair(const Operand& r, const Operand& c, G::Params p, int nsm, cudaStre
   p.tiles = (int)(p.tiles_r * parts(p.cols, BN));
   return launch_pair<G::F16, BN, R_MN, false, EPI>(r, c, p, nsm, st);
 }
-// As for the symmetric products: pairs from a quarter (from an eighth 1024 x 2048 takes 188 us instead of 175, from a half
-// 2048^2 325 instead of 303), and not for 128 rows or fewer (64 of 128 x 128: 91 us against 155).  Single blocks take 64
+// As for the symmetric products: pairs from a quarter (from an eighth 1024 x 2048 takes 168 us instead of 143, from a half
+// 2048^2 275 instead of 272), and not for 128 rows or fewer (64 of 128 x 128: 91 us against 155).  Single blocks take 64
 // columns up to two blocks an SM (16 of 333 x 130: 119 us, up to one block an SM 136), else 128 (300 of 96 x 40: 209 us
 // against 219).
 template <int EPI, bool R_MN>
@@ -381,8 +381,8 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
 }
 
 // Whether the first two steps are worth doing at once: with B1 = B(P1), P2 = B1 P1 B1 and B2 = B(P2), X <- (B2 B1) X takes
-// one Gram matrix of X and one product with X (two passes) instead of two, for three more products of the shorter
-// side's size (1536 x 6145: 510 us against 566; 2048 x 8192: 772 against 820).  Estimated from measured times: 5 us for
+// one Gram matrix of X and one product with X instead of two, for three more products of the shorter
+// side's size (1536 x 6145: 456 us against 494; 8192 x 2048: 650 against 720).  Estimated from measured times: 5 us for
 // each product's beginning and end, and 1.3, 1.6 and 0.9 PFLOP/s for Gram matrices (whole flops), products with X and
 // small symmetric products.
 // Only the first two, and from 512 rows on.  A rounding N of P turns a direction of eigenvalue t into others by
@@ -392,7 +392,7 @@ int run_iter(const Operand& r, const Operand& c, const G::Params& p, int nsm, cu
 bool worth_pairing(const Shape2& sh) {
   if (std::min(sh.rows, sh.cols) < 512) return false;
   const double m = (double)std::min(sh.rows, sh.cols), n = (double)std::max(sh.rows, sh.cols), b = (double)sh.batch;
-  const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 4 / 1.6e15);
+  const double saved = 10.0 + 1e6 * b * m * m * n * (1 / 1.3e15 + 2 / 1.6e15);
   return saved > 1.1 * 3.0 * (5.0 + 1e6 * b * m * m * m / 0.9e15);
 }
 
@@ -436,8 +436,8 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
   u.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts(items, 8), parts(8 * nsm, sh.batch)));
   const bool pairing = steps > 1 && worth_pairing(sh);
   // The product with X_s reads its second plane unless what one plane leaves out can grow at most four times in the steps
-  // that are left (Muon's last step: 3.4): a result of rank 1, 512 x 512, is off by 0.2e-3 with both planes in all five
-  // steps, 1.1e-3 in all but the last, 2.6e-3 in all but the last two, 0.15 in none.
+  // that are left (Muon's last step: 3.4): a result of rank 1, 512 x 512, is off by 0.9e-3 with both planes in all five
+  // steps, 1.4e-3 in all but the last, 2.9e-3 in all but the last two, 0.15 in none.
   const bool all = precise || m < 32, gram_all = precise || (all && std::max(sh.rows, sh.cols) < 1024);
   bool both[kMaxSteps];
   double gain = 1.0;
@@ -445,9 +445,11 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
     gain *= it.reach[s];
     both[s] = all || gain > 4.0;
   }
+  const bool across = !all && m >= 512;   // see kIterScale
+  const int sq_planes = across ? 3 : 2;
   const G::Second squares = all ? G::ALL : G::DIAGONAL;
   __half *x0, *x1, *pp, *bb, *tt;
-  const int64_t next = up(sh.batch * 2 * np, 128);   // from one square matrix to the next
+  const int64_t next = up(sh.batch * sq_planes * np, 128);   // from one square matrix to the next
   double* partial;
   auto layout = [&](Arena& ar) {
     partial = ar.take<double>((size_t)(sh.batch * u.parts));
@@ -473,8 +475,10 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
   if (!all) {
     u.squares = pp + np;
     u.ld_s = ld_p;
-    u.batch_s = 2 * np;
+    u.plane_s = np;
+    u.batch_s = sq_planes * np;
     u.next_s = next;
+    u.cleared = sq_planes - 1;
     u.side = (int)m;
     u.count = pairing ? 3 : 2;
   }
@@ -490,12 +494,13 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
   G::Params p{};
   p.rows = p.cols = (int)m;
   p.batch = (int)sh.batch;
-  p.planes = 2;
+  p.planes_r = p.planes_c = sq_planes;
   p.ld_out = p.ld_x = ld_p;
-  p.batch_out = p.batch_x = 2 * np;
+  p.batch_out = p.batch_x = sq_planes * np;
   p.plane_out = p.plane_x = np;
   p.second_out = squares;
-  const auto square = [&](const __half* q) { return Operand{q, m, m, ld_p, sh.batch * 2, np}; };
+  p.third_out = across ? 1 : 0;
+  const auto square = [&](const __half* q) { return Operand{q, m, m, ld_p, sh.batch * sq_planes, np}; };
   // out = B(x) with the coefficients of step s; out = x y
   const auto polynomial = [&](__half* out, const __half* x, int s) {
     G::Params q = p;
@@ -522,6 +527,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
     const Operand x{x0, sh.cols, sh.rows, ld_x, sh.batch * 2, nx};
     G::Params gram = p;
     gram.k = (int)(tall ? sh.rows : sh.cols);
+    gram.planes_r = gram.planes_c = 2;
     gram.second_r = gram.second_c = gram_all ? G::ALL : G::NONE;
     gram.out = pp;
     rc = tall ? run_sym<G::GRAM, true>(x, x, gram, nsm, st) : run_sym<G::GRAM, false>(x, x, gram, nsm, st);
@@ -529,7 +535,7 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
     if (two && ((rc = product(tt, bb, pp)) || (rc = product(pp, tt, bb)) || (rc = polynomial(tt, pp, s + 1)) ||
                 (rc = product(pp, tt, bb))))
       break;
-    const G::Second second = both[s] ? G::ALL : G::NONE;
+    const G::Second second = !both[s] ? G::NONE : across ? G::ACROSS : G::ALL;
     s += two ? 2 : 1;
     // wide: D[r = column][c = row] = sum_k X[k][r] B[c][k]; tall: sum_k B[r][k] X[c][k]
     const Operand poly = square(two ? pp : bb);
@@ -539,7 +545,8 @@ int run_newton_schulz(const Shape2& sh, Q::UpdateParams u, int g_type, const Ste
     q.cols = (int)sh.rows;
     q.k = (int)m;
     q.batch = (int)sh.batch;
-    q.planes = 2;
+    (tall ? q.planes_r : q.planes_c) = sq_planes;
+    (tall ? q.planes_c : q.planes_r) = 2;
     (tall ? q.second_r : q.second_c) = squares;
     (tall ? q.second_c : q.second_r) = second;
     if (!end) {

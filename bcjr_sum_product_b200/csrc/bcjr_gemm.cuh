@@ -54,10 +54,13 @@ enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 // of a large matrix of norm 1 are that small).
 //
 // Which second planes a product needs for a result of 8 bits:
-//   X in B X: all of it.  A rounding E of X is added to X, puts a share of |E| into
+//   X in B X: it.  A rounding E of X is added to X, puts a share of |E| into
 //     directions where X has next to nothing, and every step multiplies those by up to
 //     a = 3.4445 (485 times in five).  With one plane a result of rank 1 is off by 15 %,
-//     of rank 8 by 4 %.
+//     of rank 8 by 4 %.  With 512 rows or more B's diagonal is enough of B for it: where X
+//     has little, B is a I, and what the rest of B would make of the second plane lies
+//     among directions that X has, is not amplified and gets less with more rows (rank 1 to
+//     m / 4, m = 512: 1.5e-3 of the result instead of 1.1e-3; 256: 2.5e-3).
 //   X in X X^T: none.  It would change P by less than P's own rounding.
 //   P and B: the diagonal.  Roundings of B multiply X, so their errors stay in proportion
 //     to each direction and average out over a row, as do those of P, which only enters B.
@@ -66,14 +69,15 @@ enum OutType { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 //     a step of a (rank 1, 1536 x 6145, two steps at once: 1 %).  Of the second
 //     planes' blocks of 256 on the diagonal, zeros but for it, a product takes those of
 //     its tile's own rows: one to four blocks of k more.
-// So held, a result is within 1.4e-3 of the exact iteration in the 2-norm whatever its
+// So held, a result is within 1.6e-3 of the exact iteration in the 2-norm whatever its
 // singular values (half of that for updates of full rank).  For results of more than
 // 8 bits, and for matrices of few rows, every product takes all second planes:
 // R0 C0 + R0 C1 + R1 C0.
 constexpr float kIterScale = 4096.f;
 
-// Which part of an operand's or a result's second plane counts.
-enum Second { NONE = 0, DIAGONAL = 1, ALL = 2 };
+// Which part of an operand's or a result's second plane counts.  ACROSS: all of it, but multiplied by the other operand's
+// diagonal alone (of its first plane), which that keeps as a third plane.
+enum Second { NONE = 0, DIAGONAL = 1, ALL = 2, ACROSS = 3 };
 
 struct Params {
   int rows, cols, k;         // extents of r, c, k
@@ -82,7 +86,7 @@ struct Params {
   int batch;
   int splits;                // blocks of one tile (the cluster of tile_kernel)
   int second_r, second_c;    // Second, of the operands
-  int planes;                // of the operands of one matrix of the batch, one after the other in their maps' third dimension
+  int planes_r, planes_c;    // of one matrix of the batch, one after the other in the operands' maps' third dimension
   int band;                  // pair_kernel: tiles along r of a band
   // MX
   const uint8_t* sr;         // scales of R: sr[(r >> shift_r) * ld_sr + k / 128]
@@ -97,6 +101,7 @@ struct Params {
   int64_t batch_out, batch_x;
   int64_t plane_out, plane_x;   // from one plane to the other
   int second_out;               // Second, of the result and of x
+  int third_out;                // the result's diagonal as a third plane too (second_out DIAGONAL)
   int out_type;
   float fa, fb, fc;          // OUT: alpha; POLY: a, b, c
   float keep, rate;          // STEP
@@ -214,10 +219,15 @@ __device__ __forceinline__ void finish(const Params& p, int64_t batch, int r, in
         to += p.ld_out;
       }
       if (diagonal && (unsigned)(r - c0) < (unsigned)min(W, n)) {
-        float left = 0.f;
+        float left = 0.f, first = 0.f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) left = i == r - c0 ? v[i] - __half2float(h[i]) : left;
-        out[p.plane_out + (int64_t)r * p.ld_out + r] = __float2half_rn(left);
+        for (int i = 0; i < W; ++i) {
+          left = i == r - c0 ? v[i] - __half2float(h[i]) : left;
+          first = i == r - c0 ? __half2float(h[i]) : first;
+        }
+        __half* at = out + p.plane_out + (int64_t)r * p.ld_out + r;
+        *at = __float2half_rn(left);
+        if (p.third_out) at[p.plane_out] = __float2half_rn(first);
       }
     }
   } else {   // STEP
@@ -264,7 +274,8 @@ __device__ __forceinline__ uint4 scale_words(const uint8_t* s, int64_t ld, int s
 }
 
 // The blocks of k of a tile at row r0 and column c0 (of the pair's whole tile): all of k; then again, for what counts of
-// C's second plane; then of R's.  On the diagonal, that is where k is one of the tile's own columns or rows.
+// C's second plane; then of R's.  On the diagonal, that is where k is one of the tile's own columns or rows, across
+// where it is on the other operand's.
 template <int KIND, int TR, int TC>
 struct Blocks {
   int all, first_c, in_c, first_r, in_r;
@@ -273,12 +284,18 @@ struct Blocks {
     if (p.second_c == DIAGONAL) {
       first_c = c0 / 64;
       in_c = min(TC / 64, blocks - first_c);
+    } else if (p.second_c == ACROSS) {
+      first_c = r0 / 64;
+      in_c = min(TR / 64, blocks - first_c);
     } else if (p.second_c == ALL) {
       in_c = blocks;
     }
     if (p.second_r == DIAGONAL) {
       first_r = r0 / 64;
       in_r = min(TR / 64, blocks - first_r);
+    } else if (p.second_r == ACROSS) {
+      first_r = c0 / 64;
+      in_r = min(TC / 64, blocks - first_r);
     } else if (p.second_r == ALL) {
       in_r = blocks;
     }
@@ -286,16 +303,19 @@ struct Blocks {
   __device__ __forceinline__ int total() const { return all + in_c + in_r; }
   // The first value of k of block kb, the third coordinates of R and C in their maps.
   __device__ __forceinline__ void place(const Params& p, int kb, int batch, int* k, int* zr, int* zc) const {
-    *zr = *zc = batch * p.planes;
+    *zr = batch * p.planes_r;
+    *zc = batch * p.planes_c;
     int b = kb;
     if (KIND == F16 && kb >= all) {
       b = kb - all;
       if (b < in_c) {
         b += first_c;
-        ++*zc;
+        *zc += 1;
+        if (p.second_c == ACROSS) *zr += 2;
       } else {
         b += first_r - in_c;
-        ++*zr;
+        *zr += 1;
+        if (p.second_r == ACROSS) *zc += 2;
       }
     }
     *k = b * (KIND == MX ? 128 : 64);

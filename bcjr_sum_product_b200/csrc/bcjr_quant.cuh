@@ -312,9 +312,9 @@ struct UpdateParams {
   float mu;
   int nesterov;
   float eps, scale;
-  __half* squares;         // or null: second planes of `count` square matrices [batch][side][ld_s], see norm_kernel
-  int64_t ld_s, batch_s, next_s;   // next_s: from one square matrix to the next
-  int side, count;
+  __half* squares;         // or null: planes of `count` square matrices [batch][cleared][side][ld_s], see norm_kernel
+  int64_t ld_s, plane_s, batch_s, next_s;   // next_s: from one square matrix to the next
+  int side, count, cleared;
 };
 
 // u = g + mu momentum (nesterov) or momentum, from the momentum already updated.
@@ -348,7 +348,7 @@ __device__ __forceinline__ void load_span(const UpdateParams& p, const typename 
 }
 
 // First pass: updates the momentum (in place) and leaves each block's sum of squares of u.  It also clears the blocks of
-// 256 on the diagonals of the square matrices' second planes, of which only the diagonals are ever written.
+// 256 on the diagonals of the square matrices' second (and third) planes, of which only the diagonals are ever written.
 template <int T>
 __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams p) {
   using X = typename In<T>::type;
@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(kUpdateThreads) norm_kernel(const UpdateParams
   const X* g = static_cast<const X*>(p.g) + blockIdx.y * p.batch_g;
   if (p.squares != nullptr) {
     // groups of eight: 32 of a row (fewer at the end: ld_s is a multiple of 8)
-    for (int i = blockIdx.x * kUpdateThreads + threadIdx.x; i < p.count * p.side * 32; i += gridDim.x * kUpdateThreads) {
-      const int row = i / 32, r = row % p.side, c = (r & ~255) + 8 * (i % 32);
-      __half* to = p.squares + row / p.side * p.next_s + blockIdx.y * p.batch_s + (int64_t)r * p.ld_s + c;
+    for (int i = blockIdx.x * kUpdateThreads + threadIdx.x; i < p.count * p.cleared * p.side * 32; i += gridDim.x * kUpdateThreads) {
+      const int row = i / 32, r = row % p.side, c = (r & ~255) + 8 * (i % 32), plane = row / p.side;
+      __half* to = p.squares + plane / p.cleared * p.next_s + plane % p.cleared * p.plane_s + blockIdx.y * p.batch_s + (int64_t)r * p.ld_s + c;
       if (c < p.ld_s) *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
     }
   }

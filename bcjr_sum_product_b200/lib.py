@@ -463,7 +463,7 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, coeffs: Optional[Sequence] = 
     matrices ``g`` ([rows, cols] or [batch, rows, cols]; fp32, fp16, bf16) after
     division by its Frobenius norm + eps; bf16 or fp16 of the shape of g.
     Products sum in fp32.  With the default steps a bf16 result is within about 1e-3 (at
-    most 1.5e-3) of the exact iteration in the 2-norm before it is rounded, an fp16 one
+    most 2e-3) of the exact iteration in the 2-norm before it is rounded, an fp16 one
     (three times the work) within 1e-4 if g has many directions, up to 1.1e-3 if it has
     few.  ``coeffs`` is (a, b, c), or one such triple for each step; the default is
     Muon's."""

@@ -270,7 +270,7 @@ BCJR_API int bcjr_fp8_matmul(const void* a, int a_type, int64_t ld_a, const void
  * rounding left as a second such value (22 bits).  For a bf16 out these are the
  * iterates that are multiplied (but the last, which 11 bits hold well enough) and
  * the diagonals, which keeps out within about 1e-3 of the exact iteration in the
- * 2-norm (1.5e-3 at most in Muon's five steps), less than its own rounding, whatever
+ * 2-norm (2e-3 at most in Muon's five steps), less than its own rounding, whatever
  * the singular values of G (fewer than 32 rows or columns: 22 bits throughout); for
  * an fp16 out all of them (three times the products), which leaves 1e-4
  * before it is rounded, or where few directions carry G what the fp32 sums leave

@@ -184,3 +184,25 @@ def test_power_law_spectra():
             u = orthogonal_part(g)
             finished()
             assert relative(u, ref.newton_schulz(g)) <= bound(5, False)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(3, 640, 1000), (3, 1000, 640), (2, 513, 513), (5, 512, 600), (2, 700, 530)])
+@pytest.mark.parametrize("rank", [1, 30, 300, None])
+def test_batches_of_512_rows_and_more(batch, rows, cols, rank):
+    """Where X's second plane meets B's diagonal alone: each matrix of a batch its own, in single blocks and pairs."""
+    g = torch.stack([randn(rows, cols, seed=200 + i) if rank is None else low_rank(rows, cols, rank + i, seed=200 + i) for i in range(batch)])
+    out = lib.orthogonalise(g)
+    finished()
+    assert relative(out, ref.newton_schulz(g)) <= rounded(bound(5, False), torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,cols", [(600, 900), (900, 600), (2048, 2048), (1536, 6145)])
+@pytest.mark.parametrize("coeffs", [(1.875, -1.25, 0.375), [(0.5, 0.0, 0.0), (3.0, -3.2, 1.2), (2.0, -1.5, 0.5), (1.0, 0.0, 0.0)]])
+def test_other_coefficients_of_large_matrices(rows, cols, coeffs):
+    co = coeffs if isinstance(coeffs, list) else [coeffs] * 4
+    for g in (low_rank(rows, cols, 3, seed=96), randn(rows, cols, seed=98)):
+        u = orthogonal_part(g, steps=4, coeffs=coeffs)
+        finished()
+        # as for small ones: any X whose second plane is left out may grow four times
+        tol = 3 * 4 * 2.0 ** -12 + 4 * 4 * 2.0 ** -11 / math.sqrt(3)
+        assert relative(u, ref.newton_schulz(g, 4, co)) <= tol
